@@ -59,7 +59,8 @@ typedef enum {
   MLA_ERR_WORKSPACE = 3,       /* workspace too small and cannot grow (external, or capture) */
   MLA_ERR_CUDA = 4,            /* a CUDA runtime call failed; see mla_last_error_message */
   MLA_ERR_DEVICE_BAD_PAGE = 5, /* device: a block-table entry outside [0, num_pages)   */
-  MLA_ERR_DEVICE_TIMEOUT = 6   /* device: a bounded wait gave up                        */
+  MLA_ERR_DEVICE_TIMEOUT = 6,  /* device: a bounded wait gave up                        */
+  MLA_ERR_DEVICE_BAD_POSITION = 7 /* device: a rotation position outside the table      */
 } mla_status_t;
 
 enum {
@@ -179,6 +180,108 @@ mla_status_t mla_decode_noalloc(const void* q, const void* kv_cache, const int32
                                 const int32_t* cache_seqlens, float* out, float* lse,
                                 int batch, int heads, int num_pages, int max_blocks,
                                 float softmax_scale, mla_stream_t stream);
+
+/*
+ * mla_append -- write new tokens' rows into the latent cache, the position rotation
+ * applied on the way, and rotate the same tokens' query parts.  One launch.
+ *
+ * Sequence b appends n_b tokens; cache_seqlens[b] = T_b is its length with them, so its
+ * new tokens are its last n_b cached rows, as in mla_decode_multi.  Token n (the i-th of
+ * sequence b) goes to row r = T_b - n_b + i and is rotated to position
+ * p = r + pos_offset[b]:
+ *     row r of sequence b  = [ c_kv[n] (512) | R(p) k_rope[n] (64) ]
+ *     q_out[n, h]          = R(p) q_rope[n, h]
+ * R(p) turns pair i of the 32 pairs by the angle of cos_sin[p]: (x, y) ->
+ * (x c - y s, x s + y c), computed in fp32 and rounded once to bf16.  Pair i is dims
+ * (2i, 2i + 1) if interleaved = 1, (i, i + 32) if 0.
+ *
+ * c_kv       device bf16 [tokens, 512], consecutive tokens c_kv_stride elements apart
+ * k_rope     device bf16 [tokens, 64], k_rope_stride elements apart
+ * q_rope     device bf16 [tokens, heads, 64] with strides q_stride_token, q_stride_head, or
+ *            NULL (then q_out is NULL and heads is ignored)
+ * q_out      device bf16, likewise with its own strides; may be q_rope itself with the
+ *            same strides (rotation in place), and must not overlap it otherwise
+ * cos_sin    device fp32 [max_pos, 64]: 32 cosines, then 32 sines, of each position
+ * cu_tokens  device int32 [batch + 1], ascending: sequence b's new tokens are
+ *            cu_tokens[b] .. cu_tokens[b+1] (none is allowed); tokens at or beyond
+ *            cu_tokens[batch] are padding: nothing is read into the cache or written for
+ *            them.  NULL: every sequence appends tokens / batch.
+ * pos_offset device int32 [batch], or NULL for 0 (e.g. the length of a shared prefix whose
+ *            pages are not in block_table)
+ * block_table, kv_cache, cache_seqlens: as in mla_decode (block_table NULL = contiguous)
+ * Strides are elements, multiples of 8; vectors are dense.  A token whose length, row or
+ * page id is invalid sets MLA_ERR_DEVICE_BAD_PAGE, one whose position is outside
+ * [0, max_pos) MLA_ERR_DEVICE_BAD_POSITION: no cache row is written for it and its q_out
+ * is NaN.  Two tokens given the same cache row race.
+ */
+mla_status_t mla_append(const void* c_kv, const void* k_rope, const void* q_rope, void* q_out, const float* cos_sin,
+                        const int32_t* cu_tokens, const int32_t* cache_seqlens, const int32_t* pos_offset,
+                        const int32_t* block_table, void* kv_cache, int64_t c_kv_stride, int64_t k_rope_stride,
+                        int64_t q_stride_token, int64_t q_stride_head, int64_t q_out_stride_token,
+                        int64_t q_out_stride_head, int tokens, int batch, int heads, int num_pages, int max_blocks,
+                        int max_pos, int interleaved, mla_stream_t stream);
+
+/*
+ * mla_decode_window -- absorbed decode over a sliding window and the first tokens.
+ *
+ * Query i (0 <= i < s_q) of sequence b sits at position p = T_b - s_q + i, as in
+ * mla_decode_multi, and attends to the cached tokens t <= p with
+ *     t < sinks   or   t > p - window,
+ * i.e. the last `window` tokens up to its own, and the first `sinks` tokens of the
+ * sequence.  window >= 1, sinks >= 0; a window of at least T_b is plain causal decode.
+ *
+ * q       device bf16 [batch, s_q, heads, 576]
+ * out     device bf16 [batch, s_q, heads, 512], fully overwritten: the softmax weights are
+ *         rounded to bf16 for the tensor cores, so out is given with that precision
+ *         (mla_absorb_o_bf16 takes it); sums and split partials are fp32
+ * lse     device fp32 [batch, s_q, heads], fully overwritten
+ * A query that sees no token gets out = 0, lse = -inf.  Block-table entries of pages
+ * wholly outside the sinks and every query's window are never read (such pages may have
+ * been given back), and cached rows that no query of the sequence sees may hold anything;
+ * a NaN or infinity in a row that some query of the sequence sees may reach the others.
+ * s_q, heads, kv_cache, block_table, cache_seqlens, softmax_scale, errors: as in
+ * mla_decode_multi.
+ * workspace: device memory of at least mla_decode_window_workspace_size bytes, 256-byte
+ * aligned, the caller's: calls that may overlap on the GPU (streams, captured graphs)
+ * need one each.  It holds nothing between calls.  Results depend on (batch, s_q, heads,
+ * window, sinks, cache_seqlens, the device's SM count), not on page ids or on what ran before.
+ */
+size_t mla_decode_window_workspace_size(int batch, int s_q, int heads);
+mla_status_t mla_decode_window(const void* q, const void* kv_cache, const int32_t* block_table,
+                               const int32_t* cache_seqlens, void* out, float* lse, int batch, int s_q, int heads,
+                               int num_pages, int max_blocks, int window, int sinks, float softmax_scale, void* workspace,
+                               size_t workspace_bytes, mla_stream_t stream);
+
+/*
+ * mla_decode_shared -- absorbed decode of a batch whose sequences begin with the same
+ * cached tokens (a system prompt, a document): the prefix is attended to once for all
+ * rows of the batch, packed into tiles, instead of once per sequence.
+ *
+ * The cache of sequence b is the prefix's P = prefix_len[0] tokens followed by its own
+ * T_b = cache_seqlens[b] tokens.  Query i sits at position P + T_b - s_q + i and attends
+ * to every token up to its own.
+ *
+ * kv_cache     device bf16 [num_pages, 64, 576]
+ * prefix_table device int32 [prefix_blocks]: the prefix's pages in order
+ * prefix_len   device int32 [1], 0 <= P <= prefix_blocks * 64 (read on the device only)
+ * block_table  device int32 [batch, max_blocks]: pages of each sequence's own tokens; the
+ *              first of them starts a page, whatever P is
+ * cache_seqlens device int32 [batch], the own tokens, 0 <= T_b <= max_blocks * 64
+ * q, out, lse, s_q, heads, softmax_scale, workspace, empty queries, errors: as in
+ * mla_decode_window (an invalid prefix_len makes every row NaN).
+ */
+size_t mla_decode_shared_workspace_size(int batch, int s_q, int heads);
+mla_status_t mla_decode_shared(const void* q, const void* kv_cache, const int32_t* prefix_table, const int32_t* prefix_len,
+                               const int32_t* block_table, const int32_t* cache_seqlens, void* out, float* lse, int batch,
+                               int s_q, int heads, int num_pages, int prefix_blocks, int max_blocks, float softmax_scale,
+                               void* workspace, size_t workspace_bytes, mla_stream_t stream);
+
+/*
+ * mla_absorb_o_bf16 -- mla_absorb_o for the bf16 out_latent of mla_decode_window and
+ * mla_decode_shared (device bf16 [batch, heads, 512]; fp32 accumulate, fp32 out).
+ */
+mla_status_t mla_absorb_o_bf16(const void* out_latent, const void* w_uv, float* out, int batch, int heads,
+                               mla_stream_t stream);
 
 /* Bytes of workspace mla_decode needs on the current device for these sizes. */
 size_t mla_workspace_size(int batch, int heads, int max_blocks);

@@ -15,7 +15,9 @@ import os
 import torch
 
 __all__ = [
-    "MlaError", "mla_decode", "mla_decode_multi", "mla_decode_noalloc", "mla_absorb_q", "mla_absorb_o", "mla_workspace_size", "mla_set_workspace",
+    "MlaError", "mla_decode", "mla_decode_multi", "mla_decode_noalloc", "mla_absorb_q", "mla_absorb_o", "mla_append",
+    "mla_decode_window", "mla_decode_window_workspace_size", "mla_decode_shared", "mla_decode_shared_workspace_size",
+    "mla_workspace_size", "mla_set_workspace",
     "mla_get_device_error", "mla_status_string", "mla_set_knob", "mla_get_knob", "mla_selected_decode_kernel",
     "mla_timing_enable",
     "mla_timing_read", "lib", "LIB_PATH", "KNOB", "STATUS",
@@ -25,7 +27,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmla.so")
 
 STATUS = {
     0: "MLA_OK", 1: "MLA_ERR_INVALID_ARG", 2: "MLA_ERR_UNSUPPORTED", 3: "MLA_ERR_WORKSPACE", 4: "MLA_ERR_CUDA",
-    5: "MLA_ERR_DEVICE_BAD_PAGE", 6: "MLA_ERR_DEVICE_TIMEOUT",
+    5: "MLA_ERR_DEVICE_BAD_PAGE", 6: "MLA_ERR_DEVICE_TIMEOUT", 7: "MLA_ERR_DEVICE_BAD_POSITION",
 }
 KNOB = {"num_workers": 0, "min_pages": 1, "decode_kernel": 2, "wait_limit": 3, "withhold_arrive": 4, "split_policy": 5,
         "piece_cost": 6}
@@ -46,12 +48,19 @@ def _load() -> ctypes.CDLL:
                           "(nvcc, sm_100a); there is no fallback implementation")
     L = ctypes.CDLL(LIB_PATH)
     vp, i32, f32, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+    i64 = ctypes.c_int64
     sig = {
         "mla_decode": ([vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, f32, vp], i32),
         "mla_decode_multi": ([vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, f32, vp], i32),
         "mla_decode_noalloc": ([vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, f32, vp], i32),
         "mla_absorb_q": ([vp, vp, vp, vp, i32, i32, vp], i32),
         "mla_absorb_o": ([vp, vp, vp, i32, i32, vp], i32),
+        "mla_absorb_o_bf16": ([vp, vp, vp, i32, i32, vp], i32),
+        "mla_append": ([vp] * 10 + [i64] * 6 + [i32] * 7 + [vp], i32),
+        "mla_decode_window": ([vp] * 6 + [i32] * 7 + [f32, vp, sz, vp], i32),
+        "mla_decode_window_workspace_size": ([i32, i32, i32], sz),
+        "mla_decode_shared": ([vp] * 8 + [i32] * 6 + [f32, vp, sz, vp], i32),
+        "mla_decode_shared_workspace_size": ([i32, i32, i32], sz),
         "mla_workspace_size": ([i32, i32, i32], sz),
         "mla_set_workspace": ([vp, sz], i32),
         "mla_get_device_error": ([vp], i32),
@@ -191,12 +200,158 @@ def mla_absorb_q(q_nope, q_rope, w_uk, q_out, stream=None) -> None:
 
 
 def mla_absorb_o(out_latent, w_uv, out, stream=None) -> None:
-    """out[b,h] = bf16(out_latent[b,h]) W_UV[h] (fp32 accumulate, fp32 out)."""
+    """out[b,h] = bf16(out_latent[b,h]) W_UV[h] (fp32 accumulate, fp32 out).  out_latent is
+    mla_decode's fp32, or the bf16 of mla_decode_window and mla_decode_shared (then
+    mla_absorb_o_bf16 of the C ABI runs)."""
     B, H = int(out_latent.shape[0]), int(out_latent.shape[1])
-    _need(out_latent, "out_latent", torch.float32, (B, H, D_LATENT))
+    half = out_latent.dtype == torch.bfloat16
+    _need(out_latent, "out_latent", torch.bfloat16 if half else torch.float32, (B, H, D_LATENT))
     _need(w_uv, "w_uv", torch.bfloat16, (H, D_LATENT, D_V))
     _need(out, "out", torch.float32, (B, H, D_V))
+    if half:
+        _same_device(out_latent, w_uv, out)
+        _check(lib.mla_absorb_o_bf16(out_latent.data_ptr(), w_uv.data_ptr(), out.data_ptr(), B, H, _stream(stream)))
+        return
     _check(lib.mla_absorb_o(out_latent.data_ptr(), w_uv.data_ptr(), out.data_ptr(), B, H, _stream(stream)))
+
+
+def _same_device(*tensors) -> None:
+    """The library launches on the current device: every tensor must live there."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"tensors must be on the current device cuda:{dev}, got {t.device}")
+
+
+def _rows_view(t, name, shape):
+    """A bf16 CUDA tensor of ``shape`` whose last dimension is dense; other strides are free."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.stride(-1) != 1 and t.numel():
+        raise ValueError(f"{name}'s last dimension must be dense")
+    return t.stride()
+
+
+def mla_append(c_kv, k_rope, kv_cache, block_table, cache_seqlens, cos_sin, cu_tokens=None, q_rope=None, q_out=None,
+               pos_offset=None, interleaved: bool = True, stream=None) -> None:
+    """Write new tokens' rows [c_kv | rotated k_rope] into the cache and rotate q_rope into
+    q_out (see include/mla.h).  c_kv [N,512], k_rope [N,64], q_rope and q_out [N,H,64] bf16
+    (views with other strides are taken, the last dimension dense); kv_cache and
+    block_table as in mla_decode; cache_seqlens [B] int32, lengths with the new tokens;
+    cos_sin [max_pos,64] fp32; cu_tokens [B+1] int32, or None for N / B tokens per
+    sequence; pos_offset [B] int32 or None."""
+    if c_kv.dim() != 2:
+        raise ValueError("c_kv must be [N, 512]")
+    N = int(c_kv.shape[0])
+    B = int(cache_seqlens.shape[0])
+    s_c = _rows_view(c_kv, "c_kv", (N, D_LATENT))
+    s_k = _rows_view(k_rope, "k_rope", (N, D_ROPE))
+    _need(cache_seqlens, "cache_seqlens", torch.int32, (B,))
+    _need(cos_sin, "cos_sin", torch.float32)
+    if cos_sin.dim() != 2 or cos_sin.shape[1] != D_ROPE:
+        raise ValueError("cos_sin must be [max_pos, 64]")
+    if cu_tokens is not None:
+        _need(cu_tokens, "cu_tokens", torch.int32, (B + 1,))
+    if pos_offset is not None:
+        _need(pos_offset, "pos_offset", torch.int32, (B,))
+    if (q_rope is None) != (q_out is None):
+        raise ValueError("q_rope and q_out go together")
+    H, s_q, s_o = 0, (0, 0), (0, 0)
+    if q_rope is not None:
+        if q_rope.dim() != 3:
+            raise ValueError("q_rope must be [N, H, 64]")
+        H = int(q_rope.shape[1])
+        s_q = _rows_view(q_rope, "q_rope", (N, H, D_ROPE))
+        s_o = _rows_view(q_out, "q_out", (N, H, D_ROPE))
+    max_blocks, num_pages, bt = _cache_args(kv_cache, block_table, B)
+    _same_device(c_kv, k_rope, kv_cache, block_table, cache_seqlens, cos_sin, cu_tokens, q_rope, q_out, pos_offset)
+    ptr = lambda t: None if t is None else t.data_ptr()
+    _check(lib.mla_append(c_kv.data_ptr(), k_rope.data_ptr(), ptr(q_rope), ptr(q_out), cos_sin.data_ptr(), ptr(cu_tokens),
+                          cache_seqlens.data_ptr(), ptr(pos_offset), bt, kv_cache.data_ptr(), s_c[0], s_k[0], s_q[0],
+                          s_q[1], s_o[0], s_o[1], N, B, H, num_pages, max_blocks, int(cos_sin.shape[0]),
+                          1 if interleaved else 0, _stream(stream)))
+
+
+def _query_shape(q):
+    """(B, s_q, H) of q [B,H,576] or [B,s_q,H,576], and the shape of the rows it asks for."""
+    if q.dim() == 3:
+        return (q.shape[0], 1, q.shape[1]), (q.shape[0], q.shape[1])
+    if q.dim() == 4:
+        return tuple(q.shape[:3]), tuple(q.shape[:3])
+    raise ValueError("q must be [B, H, 576] or [B, s_q, H, 576]")
+
+
+def _workspace(workspace, size, stream, device):
+    """A caller's workspace, or one from torch's allocator that the call alone uses: taken
+    on the launching stream, so its reuse is ordered after this call."""
+    if workspace is not None:
+        _need(workspace, "workspace", torch.uint8)
+        return workspace
+    if stream is None:
+        return torch.empty(size, dtype=torch.uint8, device=device)
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)))
+    with torch.cuda.stream(s):
+        return torch.empty(size, dtype=torch.uint8, device=device)
+
+
+def mla_decode_window(q, kv_cache, block_table, cache_seqlens, out, lse, softmax_scale: float, window: int,
+                      sinks: int = 0, workspace=None, stream=None) -> None:
+    """Decode over the last ``window`` tokens and the first ``sinks`` (see include/mla.h).
+    q [B,H,576] or [B,s_q,H,576] bf16; out like q with 512, bf16; lse fp32; the cache
+    arguments are those of mla_decode.  ``workspace``: a CUDA uint8 tensor of at least
+    mla_decode_window_workspace_size(B, s_q, H) bytes, or None to take one from torch's
+    allocator for this call."""
+    (B, SQ, H), rows = _query_shape(q)
+    _need(q, "q", torch.bfloat16, rows + (D_QK,))
+    _need(cache_seqlens, "cache_seqlens", torch.int32, (B,))
+    _need(out, "out", torch.bfloat16, rows + (D_LATENT,))
+    _need(lse, "lse", torch.float32, rows)
+    max_blocks, num_pages, bt = _cache_args(kv_cache, block_table, B)
+    _same_device(q, kv_cache, block_table, cache_seqlens, out, lse, workspace)
+    ws = _workspace(workspace, lib.mla_decode_window_workspace_size(B, SQ, H), stream, q.device)
+    _check(lib.mla_decode_window(q.data_ptr(), kv_cache.data_ptr(), bt, cache_seqlens.data_ptr(), out.data_ptr(),
+                                 lse.data_ptr(), B, SQ, H, num_pages, max_blocks, window, sinks, softmax_scale,
+                                 ws.data_ptr(), ws.numel(), _stream(stream)))
+
+
+def mla_decode_window_workspace_size(batch: int, s_q: int, heads: int) -> int:
+    return int(lib.mla_decode_window_workspace_size(batch, s_q, heads))
+
+
+def mla_decode_shared(q, kv_cache, prefix_table, prefix_len, block_table, cache_seqlens, out, lse, softmax_scale: float,
+                      workspace=None, stream=None) -> None:
+    """Decode of a batch that shares a cached prefix (see include/mla.h).  prefix_table
+    [prefix_blocks] int32 and prefix_len [1] int32 describe it, block_table
+    [B,max_blocks] and cache_seqlens [B] int32 each sequence's own tokens; q, out, lse,
+    workspace as in mla_decode_window (mla_decode_shared_workspace_size)."""
+    (B, SQ, H), rows = _query_shape(q)
+    _need(q, "q", torch.bfloat16, rows + (D_QK,))
+    _need(prefix_table, "prefix_table", torch.int32)
+    if prefix_table.dim() != 1:
+        raise ValueError("prefix_table must be [prefix_blocks]")
+    _need(prefix_len, "prefix_len", torch.int32, (1,))
+    _need(cache_seqlens, "cache_seqlens", torch.int32, (B,))
+    _need(out, "out", torch.bfloat16, rows + (D_LATENT,))
+    _need(lse, "lse", torch.float32, rows)
+    if block_table is None:
+        raise ValueError("block_table is needed: the shared prefix and the own tokens are pages of one cache")
+    max_blocks, num_pages, bt = _cache_args(kv_cache, block_table, B)
+    _same_device(q, kv_cache, prefix_table, prefix_len, block_table, cache_seqlens, out, lse, workspace)
+    ws = _workspace(workspace, lib.mla_decode_shared_workspace_size(B, SQ, H), stream, q.device)
+    _check(lib.mla_decode_shared(q.data_ptr(), kv_cache.data_ptr(), prefix_table.data_ptr(), prefix_len.data_ptr(), bt,
+                                 cache_seqlens.data_ptr(), out.data_ptr(), lse.data_ptr(), B, SQ, H, num_pages,
+                                 prefix_table.shape[0], max_blocks, softmax_scale, ws.data_ptr(), ws.numel(),
+                                 _stream(stream)))
+
+
+def mla_decode_shared_workspace_size(batch: int, s_q: int, heads: int) -> int:
+    return int(lib.mla_decode_shared_workspace_size(batch, s_q, heads))
 
 
 def mla_workspace_size(batch: int, heads: int, max_blocks: int) -> int:

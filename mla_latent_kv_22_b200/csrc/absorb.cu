@@ -494,6 +494,157 @@ __global__ void __launch_bounds__(kOThreads, 1)
   }
 }
 
+// ================================================================ absorb_o of a bf16 latent
+// out[b,h,:] = x[b,h,:] W_UV[h] with x already bf16 (the window and shared-prefix decodes'
+// output), taken transposed: D = out^T[128 v x N rows], A = W_UV[h]^T (MN-major boxes of
+// [64 k x 64 v]), B = x (K-major, N batch rows).  Bound by HBM (W_UV and x once): with the
+// batch as N, a short batch costs no padding, and chunks of 64 k (16 KB of W_UV and N rows
+// of x) run through one ring across items, so one item's loads fly under the previous
+// one's MMAs and stores.  An item is a head, a tile of N batch rows (16 to 128) and, when
+// there are too few heads to give every SM one, one half of the 128 v dims (kHalf: M = 64).
+constexpr int kXThreads = 192;
+constexpr int kXW = 16384;           // 64 k x 128 v of W_UV
+constexpr int kXMaxStages = 11;
+constexpr int kXSmem = 229376;
+constexpr int kXChunks = kDLatent / 64;
+enum XBar { kXFull = 0, kXEmpty = kXFull + kXMaxStages, kXDFull = kXEmpty + kXMaxStages, kXDEmpty = kXDFull + 2, kXDone = kXDEmpty + 2, kXNumBars };
+
+template <bool kHalf>
+__global__ void __launch_bounds__(kXThreads, 1)
+    absorb_o_bf16_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
+                         float* __restrict__ out, int B, int H, int N, int stages, int* err, uint64_t limit_ns) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bars[kXNumBars];
+  __shared__ uint32_t tmem_s;
+  __shared__ int abort_s;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  auto bar = [&](int i) { return smem_u32(&bars[i]); };
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int kParts = kHalf ? 2 : 1, kM = 128 / kParts;
+  constexpr int kWBytes = kXW / kParts;
+  const int stage_bytes = kWBytes + N * 128;
+  const int items = H * kParts * ((B + N - 1) / N);
+
+  if (tid == 0) {
+    abort_s = 0;
+    for (int i = 0; i < stages; ++i) {
+      mbar_init(bar(kXFull + i), 1);
+      mbar_init(bar(kXEmpty + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(kXDFull + i), 1);
+      mbar_init(bar(kXDEmpty + i), 4);
+    }
+    mbar_init(bar(kXDone), 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&map_x);
+    tma_prefetch_desc(&map_w);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&tmem_s), 256);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (tid == 0) grid_dep_launch_dependents();
+  grid_dep_wait();
+  const uint32_t tmem = tmem_s;
+  const Guard gd{err, &abort_s, limit_ns};
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- TMA loads
+    if (lane == 0) {
+      int s = 0, issued = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int item = blockIdx.x; ok && item < items; item += gridDim.x) {
+        const int hp = item % (H * kParts), h = hp / kParts, v0 = kM * (hp % kParts), b0 = (item / (H * kParts)) * N;
+        for (int c = 0; c < kXChunks; ++c) {
+          if (!wait_on(bar(kXEmpty + s), phase ^ 1, gd)) { ok = false; break; }
+          const uint32_t st = sbase + s * stage_bytes;
+          mbar_expect_tx(bar(kXFull + s), stage_bytes);
+          for (int v = 0; v < kM; v += 64) tma_load_3d(st + v * 128, &map_w, v0 + v, 64 * c, h, bar(kXFull + s));
+          tma_load_3d(st + kWBytes, &map_x, 64 * c, h, b0, bar(kXFull + s));
+          ++issued;
+          if (++s == stages) {
+            s = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      // Every load issued lands before the CTA may exit (bounded).
+      for (int k = 1; k <= stages && k <= issued; ++k) {
+        const int l = issued - k;
+        drain_on(bar(kXFull + l % stages), (l / stages) & 1, limit_ns);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA issue
+    const uint32_t idesc = idesc_bf16_f32(kM, N, 1, 0);
+    constexpr uint64_t kKMajor = desc_sw128_const(16, 1024), kMNMajor = desc_sw128_const(8192, 1024);
+    int s = 0, it = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int item = blockIdx.x; ok && item < items; item += gridDim.x, ++it) {
+      const int d = it & 1;
+      ok = __all_sync(0xffffffffu, wait_on(bar(kXDEmpty + d), ((it >> 1) & 1) ^ 1, gd));
+      for (int c = 0; ok && c < kXChunks; ++c) {
+        ok = __all_sync(0xffffffffu, wait_on(bar(kXFull + s), phase, gd));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t st = sbase + s * stage_bytes;
+        mma_x4_elect<128, 2>(tmem + d * 128, kMNMajor | desc_addr(st), kKMajor | desc_addr(st + kWBytes), idesc, c > 0);
+        mma_commit_elect(bar(kXEmpty + s));
+        if (++s == stages) {
+          s = 0;
+          phase ^= 1;
+        }
+      }
+      if (ok) mma_commit_elect(bar(kXDFull + d));
+    }
+    mma_commit_elect(bar(kXDone));
+    drain_on(bar(kXDone), 0, limit_ns);
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------------- epilogue: lane = v
+    // D's rows sit in lanes 0-127, or, for M = 64, in the lower 16 lanes of each quadrant.
+    const int q = warp & 3;
+    const int v = kHalf ? 16 * q + (lane & 15) : 32 * q + lane;
+    const bool live = !kHalf || lane < 16;
+    const uint32_t t_row = tmem + ((uint32_t)(32 * q) << 16);
+    int it = 0;
+    for (int item = blockIdx.x; item < items; item += gridDim.x, ++it) {
+      const int hp = item % (H * kParts), h = hp / kParts, v0 = kM * (hp % kParts), b0 = (item / (H * kParts)) * N;
+      const int d = it & 1;
+      if (!__all_sync(0xffffffffu, wait_on(bar(kXDFull + d), (it >> 1) & 1, gd))) break;
+      tc_fence_after();
+      float* dst = out + ((size_t)b0 * H + h) * MLA_D_V + v0 + v;
+      const int rows = min(N, B - b0);
+      for (int c = 0; c < rows; c += 16) {
+        uint32_t r[16];
+        tmem_ld16(t_row + d * 128 + c, r);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (live && c + e < rows) dst[(size_t)(c + e) * H * MLA_D_V] = __uint_as_float(r[e]);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kXDEmpty + d));
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 256);
+  }
+}
+
 // ---------------------------------------------------------------- host side
 PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
@@ -590,6 +741,36 @@ cudaError_t launch_absorb_o(const float* out_latent, const __nv_bfloat16* w_uv, 
   const int grid = items < sm_count() ? items : sm_count();
   return launch_dependent(absorb_o_tc_kernel, grid, kOThreads, smem, stream, mf, mw, mo, batch, heads, err,
                           2000ull * 1000000ull);
+}
+
+template <bool kHalf>
+static cudaError_t launch_absorb_o_bf16_as(const CUtensorMap& mx, const CUtensorMap& mw, float* out, int batch, int heads,
+                                           int rows, int* err, cudaStream_t stream) {
+  static bool done[64] = {};
+  cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void*>(absorb_o_bf16_kernel<kHalf>), kXSmem + 1024, done);
+  if (e != cudaSuccess) return e;
+  const int parts = kHalf ? 2 : 1;
+  const int items = heads * parts * ((batch + rows - 1) / rows);
+  const int fit = kXSmem / (kXW / parts + rows * 128), stages = fit < kXMaxStages ? fit : kXMaxStages;
+  return launch_dependent(absorb_o_bf16_kernel<kHalf>, items < sm_count() ? items : sm_count(), kXThreads, kXSmem + 1024,
+                          stream, mx, mw, out, batch, heads, rows, stages, err, 2000ull * 1000000ull);
+}
+
+cudaError_t launch_absorb_o_bf16(const __nv_bfloat16* out_latent, const __nv_bfloat16* w_uv, float* out, int batch,
+                                 int heads, int* err, cudaStream_t stream) {
+  CUtensorMap mx, mw;
+  const uint64_t H = heads, Bn = batch;
+  const auto bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  const int rows = batch <= 16 ? 16 : batch <= 32 ? 32 : batch <= 64 ? 64 : 128;
+  if (!map3d(&mx, bf, out_latent, kDLatent, H, Bn, kDLatent * 2, H * kDLatent * 2, 64, 1, rows, sw) ||
+      !map3d(&mw, bf, w_uv, MLA_D_V, kDLatent, H, MLA_D_V * 2, (uint64_t)kDLatent * MLA_D_V * 2, 64, 64, 1, sw))
+    return cudaErrorInvalidValue;
+  // Half items when even they leave SMs without one: the loads of an item (128 KB of W_UV)
+  // are then shared by two SMs.
+  const int items = heads * ((batch + rows - 1) / rows);
+  return 2 * items <= sm_count() ? launch_absorb_o_bf16_as<true>(mx, mw, out, batch, heads, rows, err, stream)
+                                 : launch_absorb_o_bf16_as<false>(mx, mw, out, batch, heads, rows, err, stream);
 }
 
 }  // namespace mla

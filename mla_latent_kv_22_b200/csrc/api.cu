@@ -200,6 +200,7 @@ const char* mla_status_string(mla_status_t s) {
     case MLA_ERR_CUDA: return "MLA_ERR_CUDA";
     case MLA_ERR_DEVICE_BAD_PAGE: return "MLA_ERR_DEVICE_BAD_PAGE";
     case MLA_ERR_DEVICE_TIMEOUT: return "MLA_ERR_DEVICE_TIMEOUT";
+    case MLA_ERR_DEVICE_BAD_POSITION: return "MLA_ERR_DEVICE_BAD_POSITION";
   }
   return "MLA_ERR_UNKNOWN";
 }
@@ -268,7 +269,9 @@ mla_status_t mla_get_device_error(mla_stream_t stream) {
   e = cudaMemcpy(d->err, &zero, sizeof(int), cudaMemcpyHostToDevice);
   if (e != cudaSuccess) return cuda_fail(e, "clear error word");
   if (v == 0) return MLA_OK;
-  return v == MLA_ERR_DEVICE_TIMEOUT ? MLA_ERR_DEVICE_TIMEOUT : MLA_ERR_DEVICE_BAD_PAGE;
+  return v == MLA_ERR_DEVICE_TIMEOUT        ? MLA_ERR_DEVICE_TIMEOUT
+         : v == MLA_ERR_DEVICE_BAD_POSITION ? MLA_ERR_DEVICE_BAD_POSITION
+                                            : MLA_ERR_DEVICE_BAD_PAGE;
 }
 
 }  // extern "C"
@@ -453,6 +456,225 @@ mla_status_t mla_timing_read(float ms[3], int* calls) {
   }
   d->timed_calls = 0;
   return MLA_OK;
+}
+
+}  // extern "C"
+
+namespace mla {
+namespace {
+
+constexpr long long kMaxPages = ((1LL << 31) - 1) / MLA_PAGE_TOKENS - 1;  // 32-bit cache row coordinates
+
+// Sizes of a window or shared-prefix decode that every entry point checks alike.
+mla_status_t tile_sizes(int batch, int s_q, int heads) {
+  if (batch < 0 || s_q < 1 || heads < 0)
+    return fail(MLA_ERR_INVALID_ARG, "batch = %d, s_q = %d, heads = %d", batch, s_q, heads);
+  if (heads < 1 || heads > MLA_MAX_HEADS) return fail(MLA_ERR_UNSUPPORTED, "heads = %d outside [1, 128]", heads);
+  if ((long long)s_q * heads > kMaxRows)
+    return fail(MLA_ERR_UNSUPPORTED, "s_q x heads = %lld rows > %d", (long long)s_q * heads, kMaxRows);
+  if ((long long)batch * s_q * heads > (1LL << 30))
+    return fail(MLA_ERR_UNSUPPORTED, "batch x s_q x heads = %lld rows > 2^30", (long long)batch * s_q * heads);
+  return MLA_OK;
+}
+
+// The workspace bytes of a call on the current device, 0 for sizes it would reject.
+size_t tile_workspace(int batch, int s_q, int heads, bool shared) {
+  if (batch <= 0 || tile_sizes(batch, s_q, heads) != MLA_OK) return 0;
+  std::lock_guard<std::mutex> lk(g_mu);
+  DeviceState* d = nullptr;
+  if (device_state(&d) != MLA_OK) return 0;
+  static const int32_t some = 0;
+  TileArgs a{};
+  a.batch = batch;
+  a.rows = s_q * heads;
+  a.prefix_len = shared ? &some : nullptr;
+  return plan_tile(&a, d->sm_count, g_knobs[MLA_KNOB_NUM_WORKERS].load(), nullptr);
+}
+
+// The checks and launch common to both; `a` holds the call's arguments.
+mla_status_t tile_call(TileArgs& a, void* workspace, size_t workspace_bytes, mla_stream_t stream_) {
+  const bool shared = a.prefix_len != nullptr;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  if (a.max_blocks < 1) return fail(MLA_ERR_INVALID_ARG, "max_blocks must be >= 1");
+  if (a.block_table && a.num_pages < 1) return fail(MLA_ERR_INVALID_ARG, "paged cache with num_pages < 1");
+  if (a.num_pages > kMaxPages || (!a.block_table && (long long)a.batch * a.max_blocks > kMaxPages) ||
+      (long long)a.batch * a.max_blocks > (1LL << 31) - 1 || (long long)a.max_blocks * MLA_PAGE_TOKENS > (1LL << 30) ||
+      (long long)a.prefix_blocks * MLA_PAGE_TOKENS > (1LL << 30))
+    return fail(MLA_ERR_UNSUPPORTED, "cache too large for 32-bit page indexing");
+  if (!aligned16(a.q) || !aligned16(a.kv) || !aligned16(a.out))
+    return fail(MLA_ERR_INVALID_ARG, "q, kv_cache and out must be 16-byte aligned");
+  if (((reinterpret_cast<uintptr_t>(a.block_table) | reinterpret_cast<uintptr_t>(a.seqlens) |
+        reinterpret_cast<uintptr_t>(a.lse) | reinterpret_cast<uintptr_t>(a.prefix_table) |
+        reinterpret_cast<uintptr_t>(a.prefix_len)) & 3u))
+    return fail(MLA_ERR_INVALID_ARG, "int32/fp32 arrays must be 4-byte aligned");
+  if (!std::isfinite(a.scale)) return fail(MLA_ERR_INVALID_ARG, "softmax_scale is not finite");
+  if (!workspace) return fail(MLA_ERR_WORKSPACE, "workspace is null");
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u) return fail(MLA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+
+  std::lock_guard<std::mutex> lk(g_mu);
+  DeviceState* d = nullptr;
+  mla_status_t s = device_state(&d);
+  if (s != MLA_OK) return s;
+  const size_t need = plan_tile(&a, d->sm_count, g_knobs[MLA_KNOB_NUM_WORKERS].load(), workspace);
+  if (workspace_bytes < need)
+    return fail(MLA_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu bytes needed", workspace_bytes, need);
+  tile_schedule(&a);
+  // The schedule's units (pages, and a fixed cost per task) are counted in 32 bits.
+  const long long units = shared ? (long long)a.tiles * ((long long)a.prefix_blocks + kMaxPieceCost) +
+                                       (long long)a.batch * a.groups * ((long long)a.max_blocks + kMaxPieceCost)
+                                 : (long long)a.batch * ((long long)a.max_blocks + kMaxPieceCost);
+  if (units > (1LL << 31) - 1) return fail(MLA_ERR_UNSUPPORTED, "batch too large for the 32-bit split schedule");
+  a.err = d->err;
+  const int wl = g_knobs[MLA_KNOB_WAIT_LIMIT].load();
+  a.wait_limit = wl > 0 ? wl : 2000;  // ms
+  a.withhold_arrive = g_knobs[MLA_KNOB_WITHHOLD_ARRIVE].load();
+  cudaError_t e = launch_decode_tile(a, stream);
+  return e == cudaSuccess ? MLA_OK : cuda_fail(e, "decode launch");
+}
+
+}  // namespace
+}  // namespace mla
+
+extern "C" {
+
+size_t mla_decode_window_workspace_size(int batch, int s_q, int heads) { return tile_workspace(batch, s_q, heads, false); }
+size_t mla_decode_shared_workspace_size(int batch, int s_q, int heads) { return tile_workspace(batch, s_q, heads, true); }
+
+mla_status_t mla_decode_window(const void* q, const void* kv_cache, const int32_t* block_table,
+                               const int32_t* cache_seqlens, void* out, float* lse, int batch, int s_q, int heads,
+                               int num_pages, int max_blocks, int window, int sinks, float softmax_scale, void* workspace,
+                               size_t workspace_bytes, mla_stream_t stream) {
+  mla_status_t s = tile_sizes(batch, s_q, heads);
+  if (s != MLA_OK) return s;
+  if (max_blocks < 0 || num_pages < 0) return fail(MLA_ERR_INVALID_ARG, "negative size");
+  if (window < 1 || sinks < 0) return fail(MLA_ERR_INVALID_ARG, "window = %d (at least 1), sinks = %d (at least 0)", window, sinks);
+  if (batch == 0) return MLA_OK;
+  if (!q || !kv_cache || !cache_seqlens || !out || !lse) return fail(MLA_ERR_INVALID_ARG, "null pointer argument");
+  TileArgs a{};
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.kv = static_cast<const __nv_bfloat16*>(kv_cache);
+  a.block_table = block_table;
+  a.seqlens = cache_seqlens;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.lse = lse;
+  a.batch = batch;
+  a.s_q = s_q;
+  a.heads = heads;
+  a.rows = s_q * heads;
+  a.num_pages = num_pages;
+  a.max_blocks = max_blocks;
+  a.window = std::min(window, 1 << 30);  // as long as any sequence
+  a.sinks = std::min(sinks, 1 << 30);
+  a.scale = softmax_scale;
+  return tile_call(a, workspace, workspace_bytes, stream);
+}
+
+mla_status_t mla_decode_shared(const void* q, const void* kv_cache, const int32_t* prefix_table, const int32_t* prefix_len,
+                               const int32_t* block_table, const int32_t* cache_seqlens, void* out, float* lse, int batch,
+                               int s_q, int heads, int num_pages, int prefix_blocks, int max_blocks, float softmax_scale,
+                               void* workspace, size_t workspace_bytes, mla_stream_t stream) {
+  mla_status_t s = tile_sizes(batch, s_q, heads);
+  if (s != MLA_OK) return s;
+  if (max_blocks < 0 || num_pages < 0 || prefix_blocks < 0) return fail(MLA_ERR_INVALID_ARG, "negative size");
+  if (batch == 0) return MLA_OK;
+  if (!q || !kv_cache || !prefix_table || !prefix_len || !block_table || !cache_seqlens || !out || !lse)
+    return fail(MLA_ERR_INVALID_ARG, "null pointer argument");
+  if (prefix_blocks < 1) return fail(MLA_ERR_INVALID_ARG, "prefix_blocks must be >= 1");
+  TileArgs a{};
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.kv = static_cast<const __nv_bfloat16*>(kv_cache);
+  a.block_table = block_table;
+  a.seqlens = cache_seqlens;
+  a.prefix_table = prefix_table;
+  a.prefix_len = prefix_len;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.lse = lse;
+  a.batch = batch;
+  a.s_q = s_q;
+  a.heads = heads;
+  a.rows = s_q * heads;
+  a.num_pages = num_pages;
+  a.max_blocks = max_blocks;
+  a.prefix_blocks = prefix_blocks;
+  a.scale = softmax_scale;
+  return tile_call(a, workspace, workspace_bytes, stream);
+}
+
+mla_status_t mla_append(const void* c_kv, const void* k_rope, const void* q_rope, void* q_out, const float* cos_sin,
+                        const int32_t* cu_tokens, const int32_t* cache_seqlens, const int32_t* pos_offset,
+                        const int32_t* block_table, void* kv_cache, int64_t c_kv_stride, int64_t k_rope_stride,
+                        int64_t q_stride_token, int64_t q_stride_head, int64_t q_out_stride_token,
+                        int64_t q_out_stride_head, int tokens, int batch, int heads, int num_pages, int max_blocks,
+                        int max_pos, int interleaved, mla_stream_t stream) {
+  if (tokens < 0 || batch < 0 || heads < 0 || num_pages < 0 || max_blocks < 0 || max_pos < 0)
+    return fail(MLA_ERR_INVALID_ARG, "negative size");
+  if (tokens == 0) return MLA_OK;
+  if (batch < 1) return fail(MLA_ERR_INVALID_ARG, "%d tokens of no sequence", tokens);
+  if (!c_kv || !k_rope || !cos_sin || !cache_seqlens || !kv_cache) return fail(MLA_ERR_INVALID_ARG, "null pointer argument");
+  if ((q_rope != nullptr) != (q_out != nullptr)) return fail(MLA_ERR_INVALID_ARG, "q_rope and q_out go together");
+  if (q_rope && (heads < 1 || heads > MLA_MAX_HEADS)) return fail(MLA_ERR_UNSUPPORTED, "heads = %d outside [1, 128]", heads);
+  if (max_blocks < 1) return fail(MLA_ERR_INVALID_ARG, "max_blocks must be >= 1");
+  if (block_table && num_pages < 1) return fail(MLA_ERR_INVALID_ARG, "paged cache with num_pages < 1");
+  if ((long long)max_blocks * MLA_PAGE_TOKENS > (1LL << 30)) return fail(MLA_ERR_UNSUPPORTED, "cache too large for 32-bit rows");
+  if (!cu_tokens && tokens % batch)
+    return fail(MLA_ERR_INVALID_ARG, "%d tokens are not the same number for each of %d sequences (cu_tokens is null)", tokens, batch);
+  if (interleaved != 0 && interleaved != 1) return fail(MLA_ERR_INVALID_ARG, "interleaved = %d", interleaved);
+  if (!aligned16(c_kv) || !aligned16(k_rope) || !aligned16(q_rope) || !aligned16(q_out) || !aligned16(cos_sin) || !aligned16(kv_cache))
+    return fail(MLA_ERR_INVALID_ARG, "c_kv, k_rope, q_rope, q_out, cos_sin and kv_cache must be 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(cu_tokens) | reinterpret_cast<uintptr_t>(cache_seqlens) |
+       reinterpret_cast<uintptr_t>(pos_offset) | reinterpret_cast<uintptr_t>(block_table)) & 3u)
+    return fail(MLA_ERR_INVALID_ARG, "int32 arrays must be 4-byte aligned");
+  int64_t strides[6] = {c_kv_stride, k_rope_stride, q_stride_token, q_stride_head, q_out_stride_token, q_out_stride_head};
+  for (int i = 0; i < (q_rope ? 6 : 2); ++i)
+    if (strides[i] % 8) return fail(MLA_ERR_INVALID_ARG, "strides must be multiples of 8 elements (16 bytes)");
+
+  std::lock_guard<std::mutex> lk(g_mu);
+  DeviceState* d = nullptr;
+  mla_status_t s = device_state(&d);
+  if (s != MLA_OK) return s;
+  AppendArgs a{};
+  a.c_kv = static_cast<const __nv_bfloat16*>(c_kv);
+  a.k_rope = static_cast<const __nv_bfloat16*>(k_rope);
+  a.q_rope = static_cast<const __nv_bfloat16*>(q_rope);
+  a.q_out = static_cast<__nv_bfloat16*>(q_out);
+  a.cos_sin = cos_sin;
+  a.cu_tokens = cu_tokens;
+  a.seqlens = cache_seqlens;
+  a.pos_offset = pos_offset;
+  a.block_table = block_table;
+  a.kv = static_cast<__nv_bfloat16*>(kv_cache);
+  a.ckv_stride = c_kv_stride;
+  a.krope_stride = k_rope_stride;
+  a.q_stride_n = q_stride_token;
+  a.q_stride_h = q_stride_head;
+  a.qo_stride_n = q_out_stride_token;
+  a.qo_stride_h = q_out_stride_head;
+  a.tokens = tokens;
+  a.batch = batch;
+  a.heads = heads;
+  a.num_pages = num_pages;
+  a.max_blocks = max_blocks;
+  a.max_pos = max_pos;
+  a.err = d->err;
+  cudaError_t e = launch_append(a, interleaved != 0, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MLA_OK : cuda_fail(e, "append launch");
+}
+
+mla_status_t mla_absorb_o_bf16(const void* out_latent, const void* w_uv, float* out, int batch, int heads,
+                               mla_stream_t stream) {
+  if (batch < 0 || heads < 0) return fail(MLA_ERR_INVALID_ARG, "negative size");
+  if (batch == 0) return MLA_OK;
+  if (!out_latent || !w_uv || !out) return fail(MLA_ERR_INVALID_ARG, "null pointer argument");
+  if (heads < 1 || heads > MLA_MAX_HEADS) return fail(MLA_ERR_UNSUPPORTED, "heads = %d outside [1, 128]", heads);
+  if (!aligned16(out_latent) || !aligned16(w_uv) || !aligned16(out))
+    return fail(MLA_ERR_INVALID_ARG, "absorb_o operands must be 16-byte aligned");
+  std::lock_guard<std::mutex> lk(g_mu);
+  DeviceState* d = nullptr;
+  mla_status_t s = device_state(&d);
+  if (s != MLA_OK) return s;
+  cudaError_t e = launch_absorb_o_bf16(static_cast<const __nv_bfloat16*>(out_latent), static_cast<const __nv_bfloat16*>(w_uv),
+                                       out, batch, heads, d->err, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MLA_OK : cuda_fail(e, "absorb_o launch");
 }
 
 }  // extern "C"

@@ -1,0 +1,938 @@
+// Sliding-window and shared-prefix decode: split-KV absorbed decode with one CTA per
+// worker, a tile of N = 16, 32 or 64 query rows and one 64-token page per step.
+//
+// A page is loaded once and feeds both products from the same shared memory:
+//     S[64 x 64]    = q'[N x 576] . K^T       (M = 64 rows, N = 64 tokens, K = 576)
+//     O^T[512 x N] += V^T[512 x 64] . P^T     (four M = 128 blocks of dims, N rows, K = 64)
+// The second product is taken transposed: its accumulator is 4 N columns of tensor memory
+// instead of 512, so it fits beside S, and the page's [64 tokens x 64 dims] boxes serve as
+// the K-major B operand of the first and, read MN-major, as the A operand of the second.
+// Rows of S at or beyond N come from whatever shared memory follows q' and are never read.
+//
+// Every 64-token page costs 36 + 16 MMAs whatever the row count, under the time its 73.7 KB
+// take from HBM at 148 SMs' share of the copy rate; so few rows (a window decode on a
+// tensor-parallel shard) run at the speed of the loads, and the rows of many sequences are
+// packed into tiles of 64 where they share the tokens (a common prefix).
+//
+// Roles (256 threads).  Warp 0: page loads (TMA) into two rings, one of 16 KB slots (128
+// latent dims of a page, four per page; freed by the second product) and one of 8 KB slots
+// (the rope dims, freed by the first).  Warp 1: tensor memory and MMA issue.  Warp 2:
+// zeroes the rows of a page that no query of the sequence sees (past its end, or between
+// the sinks and the window), where a masked P of 0 would meet whatever the cache holds.
+// Warp 3: q' loads, one tile per piece.  Warps 4-7: softmax of the 16 rows in their TMEM
+// quadrant (two threads per row, 32 tokens each) and the epilogue.
+//
+// The running maximum is lazy as in decode_pair.cu: O and the sum are rescaled only when a
+// page's maximum exceeds the reference by more than 2^8.  Since O's lanes are dims, all
+// four warps rescale for a row of any of them; they meet once per page.  P is rounded to
+// bf16 (2^-9 relative) for the tensor cores; scores, sums, O and the split partials stay
+// fp32; out is rounded once to bf16.
+//
+// Every mbarrier wait is bounded by a time limit; on expiry the kernel records
+// MLA_ERR_DEVICE_TIMEOUT, drains its work in flight and returns.  No trap.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+
+#include "mla_device.cuh"
+#include "mla_internal.h"
+#include "sm100_ptx.cuh"
+#include "worker_range.cuh"
+
+namespace mla {
+namespace {
+
+using namespace sm100;
+
+constexpr int kThreads = 256;
+constexpr int kBox = 8192;            // [64 tokens x 64 bf16], 128B swizzle
+constexpr int kSlotBytes = 2 * kBox;  // a latent slot: 128 dims of a page
+constexpr int kPageSlots = 4;
+constexpr float kRescaleThreshold = 8.0f;  // log2 units
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColO = 0, kColS = 256;  // O^T: block m at 4 columns-of-N m; S: two buffers of 64 columns
+
+// Shared memory for a row tile of N: q' (9 boxes of [N rows x 64 dims]), P (two buffers of
+// [N rows x 64 tokens]), the rope ring and the latent ring.
+template <int N>
+struct Layout {
+  static constexpr int kQBox = N * 128;
+  static constexpr int kRopeSlots = N == 64 ? 1 : 3;
+  static constexpr int kSlots = N == 64 ? 8 : N == 32 ? 9 : 11;
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffP = 9 * kQBox;
+  static constexpr int kOffRope = kOffP + 2 * kQBox;
+  static constexpr int kOffRing = kOffRope + kRopeSlots * kBox;
+  static constexpr int kBytes = kOffRing + kSlots * kSlotBytes;
+  static constexpr int kAlloc = kBytes + 1024;  // + alignment slack
+  static_assert(N == 16 || N == 32 || N == 64, "row tile");
+  // The first product reads 64 rows of every q' box; the last box's reach stays inside.
+  static_assert(8 * kQBox + 64 * 128 <= kBytes, "q' rows read outside the allocation");
+  static_assert(kQBox % 1024 == 0 && kOffRope % 1024 == 0 && kOffRing % 1024 == 0, "1024-byte tiles");
+  static_assert(kAlloc + 2048 <= 232448, "dynamic + static shared memory above the per-CTA limit");
+  static_assert(4 * N <= 256 && kColS + 128 <= kTmemCols, "tensor-memory regions overlap");
+};
+constexpr int kMaxSlots = 11, kMaxRope = 3;
+
+enum Bar {
+  kFull = 0,                     // [slot] a latent slot landed (and, if dirty, was cleaned)
+  kEmpty = kFull + kMaxSlots,    // [slot] the second product has read it
+  kDirty = kEmpty + kMaxSlots,   // [slot] a latent slot with unseen rows landed
+  kRFull = kDirty + kMaxSlots,   // [rope slot]
+  kREmpty = kRFull + kMaxRope,   // [rope slot]
+  kQFull = kREmpty + kMaxRope,
+  kQEmpty,                       // the piece's last first product has read q'
+  kSFull,                        // [2] scores of a page are in S
+  kSFree = kSFull + 2,           // [2] the 4 softmax warps have read them
+  kPFull = kSFree + 2,           // [2] the 4 softmax warps wrote P (and rescaled O)
+  kODone = kPFull + 2,           // [2] the second product of a page is done
+  kOFree = kODone + 2,           // the 4 softmax warps read O in the epilogue
+  kMeet,                         // the 4 softmax warps met
+  kDrain,
+  kNumBars
+};
+
+__device__ __forceinline__ uint64_t now_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+
+struct Ctl {
+  int* err;
+  volatile int* abort;
+  uint64_t limit_ns;
+};
+
+__device__ __noinline__ void wait_timed_out(int* err, volatile int* abort) {
+  set_device_error(err, MLA_ERR_DEVICE_TIMEOUT);
+  *abort = 1;
+}
+
+// Bounded wait on an mbarrier phase; false on timeout (recorded) or abort.
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const Ctl& c) {
+  if (mbar_try_wait_cta(bar, parity)) return true;
+  uint64_t t0 = 0;
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait_cta(bar, parity)) return true;
+    if ((i & 63) == 0) {
+      if (*c.abort) return false;
+      const uint64_t t = now_ns();
+      if (t0 == 0) {
+        t0 = t;
+      } else if (t - t0 > c.limit_ns) {
+        wait_timed_out(c.err, c.abort);
+        return false;
+      }
+    }
+  }
+}
+__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, const Ctl& c) {
+  return __all_sync(0xffffffffu, wait_bar(bar, parity, c));
+}
+__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+  const uint64_t t0 = now_ns();
+  while (!mbar_try_wait_cta(bar, parity) && now_ns() - t0 < limit_ns) {
+  }
+}
+
+// ---------------------------------------------------------------- tasks
+// The pages of a task: page p of its list is page real(p) of its table; the first `ns`
+// hold the sinks, the rest run from the window's first page to the last.
+struct Span {
+  int T, n, ns, skip;
+  int hole0, hole1;  // tokens [hole0, hole1) are in no query's sight (between sinks and window)
+  __device__ __forceinline__ int real(int p) const { return p < ns ? p : p + skip; }
+};
+
+__device__ __forceinline__ Span window_span(const TileArgs& a, int T) {
+  Span s{T, 0, 0, 0, 0, 0};
+  if (T <= 0 || T > a.max_blocks * kPage) return s;
+  const int first = max(0, T - a.s_q - a.window + 1);
+  const int sinks = min(a.sinks, T);
+  s.ns = (sinks + kPage - 1) / kPage;
+  s.skip = max(0, first / kPage - s.ns);
+  s.n = (T + kPage - 1) / kPage - s.skip;
+  s.hole0 = sinks;
+  s.hole1 = first;
+  return s;
+}
+
+template <bool kShared>
+struct TaskLengths {
+  const TileArgs* a;
+  __device__ __forceinline__ int raw(int t) const {
+    if (!kShared) return a->seqlens[t];
+    return t < a->tiles ? *a->prefix_len : a->seqlens[(t - a->tiles) / a->groups];
+  }
+  __device__ __forceinline__ int cap(int t) const { return kShared && t < a->tiles ? a->prefix_blocks : a->max_blocks; }
+  __device__ __forceinline__ bool bad(int t) const {
+    const int T = raw(t);
+    return T < 0 || T > cap(t) * kPage;
+  }
+  __device__ __forceinline__ int pages(int t) const {
+    const int T = raw(t);
+    if (!kShared) return window_span(*a, T).n;
+    return (T < 0 || T > cap(t) * kPage) ? 0 : (T + kPage - 1) / kPage;
+  }
+};
+
+struct Task {
+  Span s;
+  const int32_t* table;  // null: page = base + real
+  int base;
+  int row0, live;  // first query row of the whole batch's, rows of the tile
+  int srow;        // row0 within its sequence (window, own tokens)
+};
+
+template <int N, bool kShared>
+__device__ __forceinline__ Task load_task(const TileArgs& a, int t, int g) {
+  Task k;
+  k.base = 0;
+  if (kShared && t < a.tiles) {
+    const int T = *a.prefix_len;
+    k.s = Span{T, (T + kPage - 1) / kPage, (T + kPage - 1) / kPage, 0, 0, 0};
+    k.table = a.prefix_table;
+    k.row0 = t * N;
+    k.live = min(N, a.batch * a.rows - k.row0);
+    k.srow = 0;
+    return k;
+  }
+  const int b = kShared ? (t - a.tiles) / a.groups : t;
+  if (kShared) g = (t - a.tiles) % a.groups;
+  const int T = a.seqlens[b];
+  k.s = kShared ? Span{T, (T + kPage - 1) / kPage, (T + kPage - 1) / kPage, 0, 0, 0} : window_span(a, T);
+  k.table = a.block_table ? a.block_table + (size_t)b * a.max_blocks : nullptr;
+  k.base = b * a.max_blocks;
+  k.srow = g * N;
+  k.row0 = b * a.rows + k.srow;
+  k.live = min(N, a.rows - k.srow);
+  return k;
+}
+
+struct Piece {
+  int t, pa, pe;
+};
+
+// Iterates the pieces of a worker's range in schedule order.
+template <bool kShared>
+struct PieceIter {
+  WorkerRange rg;
+  int t;
+  __device__ explicit PieceIter(const volatile WorkerRange& r) : rg{r.b0, r.p0, r.b1, r.p1}, t(r.b0) {}
+  __device__ bool next(Piece& pc, const TileArgs& a) {
+    if (rg.b0 < 0) return false;
+    const TaskLengths<kShared> len{&a};
+    while (t <= rg.b1) {
+      const int cur = t++;
+      const int pa = cur == rg.b0 ? rg.p0 : 0;
+      const int pe = cur == rg.b1 ? rg.p1 : len.pages(cur);
+      if (pa < pe) {
+        pc = {cur, pa, pe};
+        return true;
+      }
+    }
+    return false;
+  }
+};
+
+// Whether some row of table page `real` is in no query's sight.
+__device__ __forceinline__ bool page_dirty(const Span& s, int real) {
+  const int t0 = real * kPage;
+  return s.T < t0 + kPage || (max(s.hole0, t0) < min(s.hole1, t0 + kPage));
+}
+
+// Bits [0, x) of a word.
+__device__ __forceinline__ uint32_t below(int x) { return x <= 0 ? 0u : x >= 32 ? 0xffffffffu : (1u << x) - 1u; }
+
+template <int N, bool kShared>
+__global__ void __launch_bounds__(kThreads, 1)
+    decode_tile_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap q_map,
+                       const __grid_constant__ TileArgs a, uint64_t limit_ns) {
+  using Lay = Layout<N>;
+  constexpr int kSlots = Lay::kSlots, kRope = Lay::kRopeSlots;
+  constexpr uint32_t kIdescS = idesc_bf16_f32(64, 64, 0, 0);   // A q' K-major, B rows K-major
+  constexpr uint32_t kIdescO = idesc_bf16_f32(128, N, 1, 0);   // A rows MN-major, B P K-major
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bars[kNumBars];
+  __shared__ uint32_t tmem_base_s;
+  __shared__ int abort_s;
+  __shared__ int bad_s[8];  // [piece % 8] the piece met a page id outside the cache
+  __shared__ RangeScratch range_s;
+  __shared__ float al_s[2][64];   // [page parity][row] rescale factor; epilogue: 1 / l
+  __shared__ int need_s[2][4];    // [page parity][warp]
+
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  auto bar = [&](int i) { return smem_u32(&bars[i]); };
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int w = kShared ? blockIdx.x : blockIdx.x / a.groups;
+  const int grp = kShared ? 0 : blockIdx.x % a.groups;
+  const int np = a.block_table ? a.num_pages : a.batch * a.max_blocks;
+
+  if (tid == 0) {
+    abort_s = 0;
+    for (int i = 0; i < 8; ++i) bad_s[i] = 0;
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(bar(kFull + s), 1);   // the producer, or the cleaning warp
+      mbar_init(bar(kEmpty + s), 1);  // MMA commit
+      mbar_init(bar(kDirty + s), 1);
+    }
+    for (int s = 0; s < kRope; ++s) {
+      mbar_init(bar(kRFull + s), 1);
+      mbar_init(bar(kREmpty + s), 1);
+    }
+    mbar_init(bar(kQFull), 1);
+    mbar_init(bar(kQEmpty), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(kSFull + i), 1);
+      mbar_init(bar(kSFree + i), 4);
+      mbar_init(bar(kPFull + i), 4);
+      mbar_init(bar(kODone + i), 1);
+    }
+    mbar_init(bar(kOFree), 4);
+    mbar_init(bar(kMeet), 4);
+    mbar_init(bar(kDrain), 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&kv_map);
+    tma_prefetch_desc(&q_map);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&tmem_base_s), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  // Everything above overlaps the previous grid on the stream; from here on its writes
+  // (the lengths, q', the tables, the cache) are visible.
+  grid_dep_wait();
+  derive_range(TaskLengths<kShared>{&a}, kShared ? a.tiles + a.batch * a.groups : a.batch, a.num_workers, a.min_pages, 1,
+               a.whole_slack, a.piece_cost, a.task, a.err, w, range_s);
+  const uint32_t tmem = tmem_base_s;
+  const Ctl ctl{a.err, &abort_s, limit_ns};
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ page loads
+    PieceIter<kShared> pi(range_s.rg);
+    Piece pc;
+    int slot = 0, rslot = 0, piece = 0, fills = 0;
+    uint32_t phase = 1, rphase = 1;       // parity of the "empty" phase to wait for
+    uint32_t dpar = 0;                    // [slot] parity of the slot's next dirty fill
+    uint32_t was_dirty = 0, was = 0;      // [slot] the last fill was dirty; there was one
+    uint32_t lpar = 0, rpar = 0, rwas = 0;  // [slot] parity of the last fill's "full" phase
+    int withheld = -1;
+    bool ok = true;
+    while (ok && pi.next(pc, a)) {
+      const Task k = load_task<N, kShared>(a, pc.t, grp);
+      int ids = 0, ids_at = pc.pa - 32;  // lane l holds the id of list page ids_at + l
+      for (int p = pc.pa; p < pc.pe && ok; ++p) {
+        if (p >= ids_at + 32) {
+          ids_at = p;
+          const int pp = p + lane;
+          ids = pp < pc.pe ? (k.table ? k.table[k.s.real(pp)] : k.base + k.s.real(pp)) : 0;
+          if (__any_sync(0xffffffffu, (unsigned)ids >= (unsigned)np)) {
+            if ((unsigned)ids >= (unsigned)np) set_device_error(a.err, MLA_ERR_DEVICE_BAD_PAGE);
+            if (lane == 0) *const_cast<volatile int*>(&bad_s[piece & 7]) = 1;
+            __syncwarp();
+          }
+        }
+        const int id = __shfl_sync(0xffffffffu, ids, p - ids_at);
+        const int y = (unsigned)id < (unsigned)np ? id * kPage : np * kPage;  // out of range: reads zeros
+        const bool dirty = page_dirty(k.s, k.s.real(p));
+#pragma unroll 1
+        for (int m = 0; m < kPageSlots; ++m) {
+          if (!wait_all(bar(kEmpty + slot), phase, ctl)) { ok = false; break; }
+          const uint32_t bit = 1u << slot;
+          if (lane == 0) {
+            const uint32_t b = bar((dirty ? kDirty : kFull) + slot);
+            if (a.withhold_arrive && blockIdx.x == 0 && fills == 1) {
+              withheld = slot;  // timeout test: this fill never completes
+            } else {
+              const uint32_t dst = sbase + Lay::kOffRing + slot * kSlotBytes;
+              mbar_expect_tx(b, kSlotBytes);
+              tma_load_2d(dst, &kv_map, 128 * m, y, b);
+              tma_load_2d(dst + kBox, &kv_map, 128 * m + 64, y, b);
+            }
+          }
+          if (dirty) {
+            lpar = (lpar & ~bit) | (dpar & bit);
+            dpar ^= bit;
+            was_dirty |= bit;
+          } else {
+            lpar = (lpar & ~bit) | ((phase ^ 1u) ? bit : 0u);
+            was_dirty &= ~bit;
+          }
+          was |= bit;
+          ++fills;
+          if (++slot == kSlots) {
+            slot = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok || !wait_all(bar(kREmpty + rslot), rphase, ctl)) { ok = false; break; }
+        if (lane == 0) {
+          mbar_expect_tx(bar(kRFull + rslot), kBox);
+          tma_load_2d(sbase + Lay::kOffRope + rslot * kBox, &kv_map, kDLatent, y, bar(kRFull + rslot));
+        }
+        rwas |= 1u << rslot;
+        rpar = (rpar & ~(1u << rslot)) | ((rphase ^ 1u) << rslot);
+        if (++rslot == kRope) {
+          rslot = 0;
+          rphase ^= 1u;
+        }
+      }
+      ++piece;
+    }
+    // Drain: every load issued lands before the CTA may exit (bounded).
+    if (lane == 0) {
+      for (int s = 0; s < kSlots; ++s)
+        if (((was >> s) & 1u) && s != withheld)
+          drain_wait(bar((((was_dirty >> s) & 1u) ? kDirty : kFull) + s), (lpar >> s) & 1u, limit_ns);
+      for (int s = 0; s < kRope; ++s)
+        if ((rwas >> s) & 1u) drain_wait(bar(kRFull + s), (rpar >> s) & 1u, limit_ns);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issue
+    PieceIter<kShared> pi(range_s.rg);
+    Piece pc;
+    // Descriptors: a K-major step of 16 dims is 32 bytes, an MN-major step of 16 tokens
+    // 2048 bytes; the two 64-dim boxes of a slot are the MN-major halves of 128 dims.
+    constexpr uint64_t kKMajor = desc_sw128_const(16, 1024), kMNMajor = desc_sw128_const(kBox, 1024);
+    const uint64_t dq = kKMajor | desc_addr(sbase + Lay::kOffQ);
+    const uint64_t dp = kKMajor | desc_addr(sbase + Lay::kOffP);
+    const uint64_t drope = kKMajor | desc_addr(sbase + Lay::kOffRope);
+    const uint32_t ring = desc_addr(sbase + Lay::kOffRing);
+    int slot = 0, vslot = 0, rslot = 0, piece = 0;  // next slot of the first / second product
+    uint32_t phase = 0, rphase = 0;
+    int g = 0;
+    bool ok = true;
+    // Scores of page gs into S buffer gs & 1.
+    auto do_s = [&](int gs) -> bool {
+      if (!wait_all(bar(kSFree + (gs & 1)), ((gs >> 1) & 1) ^ 1, ctl)) return false;
+      tc_fence_after();
+      const uint32_t d = tmem + kColS + 64 * (gs & 1);
+#pragma unroll 1
+      for (int m = 0; m < kPageSlots; ++m) {
+        if (!wait_all(bar(kFull + slot), phase, ctl)) return false;
+        tc_fence_after();
+        const uint64_t bk = kKMajor | (ring + slot * (kSlotBytes >> 4));
+        mma_x4_elect<2, 2>(d, dq + (2 * m) * (Lay::kQBox >> 4), bk, kIdescS, m ? 1u : 0u);
+        mma_x4_elect<2, 2>(d, dq + (2 * m + 1) * (Lay::kQBox >> 4), bk + (kBox >> 4), kIdescS, 1u);
+        if (++slot == kSlots) {
+          slot = 0;
+          phase ^= 1u;
+        }
+      }
+      if (!wait_all(bar(kRFull + rslot), rphase, ctl)) return false;
+      tc_fence_after();
+      mma_x4_elect<2, 2>(d, dq + 8 * (Lay::kQBox >> 4), drope + rslot * (kBox >> 4), kIdescS, 1u);
+      mma_commit_elect(bar(kREmpty + rslot));
+      mma_commit_elect(bar(kSFull + (gs & 1)));
+      if (++rslot == kRope) {
+        rslot = 0;
+        rphase ^= 1u;
+      }
+      return true;
+    };
+    auto do_o = [&](int gs, bool first) -> bool {
+      if (!wait_all(bar(kPFull + (gs & 1)), (gs >> 1) & 1, ctl)) return false;
+      if (first && piece > 0 && !wait_all(bar(kOFree), (piece - 1) & 1, ctl)) return false;
+      tc_fence_after();
+      const uint64_t bp = dp + (uint64_t)((gs & 1) * (Lay::kQBox >> 4));
+#pragma unroll 1
+      for (int m = 0; m < kPageSlots; ++m) {
+        const uint64_t av = kMNMajor | (ring + vslot * (kSlotBytes >> 4));
+        mma_x4_elect<128, 2>(tmem + kColO + N * m, av, bp, kIdescO, first ? 0u : 1u);
+        mma_commit_elect(bar(kEmpty + vslot));
+        if (++vslot == kSlots) vslot = 0;
+      }
+      mma_commit_elect(bar(kODone + (gs & 1)));
+      return true;
+    };
+    while (ok && pi.next(pc, a)) {
+      const int n = pc.pe - pc.pa;
+      if (!wait_all(bar(kQFull), piece & 1, ctl)) { ok = false; break; }
+      tc_fence_after();
+      for (int i = 0; i <= n && ok; ++i) {
+        bool o_done = i == 0;
+        if (i < n) {
+          // The second product of page i - 1 goes first when its P is ready before the last
+          // slot of page i: it frees the slots that further loads wait for.
+          if (i > 0) {
+            int s3 = slot + 3;
+            uint32_t p3 = phase;
+            if (s3 >= kSlots) {
+              s3 -= kSlots;
+              p3 ^= 1u;
+            }
+            const int gp = g + i - 1;
+            const uint32_t pbar = bar(kPFull + (gp & 1)), fbar = bar(kFull + s3);
+            uint64_t t0 = 0;
+            for (uint32_t it = 1;; ++it) {
+              if (__all_sync(0xffffffffu, mbar_test(pbar, (gp >> 1) & 1))) {
+                ok = do_o(gp, i == 1);
+                o_done = true;
+                break;
+              }
+              if (__all_sync(0xffffffffu, mbar_test(fbar, p3))) break;
+              if ((it & 63) == 0) {
+                const uint64_t t = now_ns();
+                if (t0 == 0) t0 = t;
+                // Past the limit, or aborted: the bounded wait that follows says so.
+                if (__any_sync(0xffffffffu, *ctl.abort || t - t0 > limit_ns)) break;
+              }
+            }
+          }
+          if (ok) ok = do_s(g + i);
+          if (ok && i == n - 1) mma_commit_elect(bar(kQEmpty));
+        }
+        if (ok && !o_done) ok = do_o(g + i - 1, i == 1);
+      }
+      g += n;
+      ++piece;
+    }
+    // Every MMA issued is done before tensor memory is released (bounded).
+    mma_commit_elect(bar(kDrain));
+    drain_wait(bar(kDrain), 0, limit_ns);
+    __syncwarp();
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ rows in no query's sight
+    PieceIter<kShared> pi(range_s.rg);
+    Piece pc;
+    int slot = 0;
+    uint32_t dpar = 0;
+    bool ok = true;
+    while (ok && pi.next(pc, a)) {
+      const Task k = load_task<N, kShared>(a, pc.t, grp);
+      for (int p = pc.pa; p < pc.pe && ok; ++p) {
+        const int real = k.s.real(p), t0 = real * kPage;
+        if (!page_dirty(k.s, real)) {
+          slot += kPageSlots;
+          if (slot >= kSlots) slot -= kSlots;
+          continue;
+        }
+        // Rows [h0, h1) and [e0, 64) of the page.
+        const int h0 = max(k.s.hole0 - t0, 0), h1 = max(h0, min(k.s.hole1 - t0, kPage));
+        const int e0 = min(max(k.s.T - t0, 0), kPage);
+        const int nrow = (h1 - h0) + (kPage - e0);
+        for (int m = 0; m < kPageSlots; ++m) {
+          if (!wait_all(bar(kDirty + slot), (dpar >> slot) & 1u, ctl)) { ok = false; break; }
+          dpar ^= 1u << slot;
+          uint8_t* st = smem + Lay::kOffRing + slot * kSlotBytes;
+          for (int idx = lane; idx < 2 * nrow * 8; idx += 32) {
+            const int box = idx / (nrow * 8), rem = idx % (nrow * 8);
+            const int r = rem / 8, row = r < h1 - h0 ? h0 + r : e0 + (r - (h1 - h0));
+            *reinterpret_cast<uint4*>(st + box * kBox + row * 128 + (rem % 8) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kFull + slot));
+          if (++slot == kSlots) slot = 0;
+        }
+      }
+    }
+  } else if (warp == 3) {
+    // ------------------------------------------------------------ q' of each piece
+    if (lane == 0) {
+      PieceIter<kShared> pi(range_s.rg);
+      Piece pc;
+      int piece = 0;
+      while (pi.next(pc, a)) {
+        const Task k = load_task<N, kShared>(a, pc.t, grp);
+        if (!wait_bar(bar(kQEmpty), (piece & 1) ^ 1, ctl)) break;
+        mbar_expect_tx(bar(kQFull), 9 * Lay::kQBox);
+        for (int d = 0; d < 9; ++d)
+          tma_load_2d(sbase + Lay::kOffQ + d * Lay::kQBox, &q_map, 64 * d, k.row0, bar(kQFull));
+        ++piece;
+      }
+      if (piece > 0) drain_wait(bar(kQFull), (piece - 1) & 1, limit_ns);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ softmax and epilogue
+    const int q = warp & 3;               // TMEM lane quadrant
+    const int half = lane >> 4;           // which 32 of the page's 64 tokens
+    const int row = 16 * q + (lane & 15); // row of the tile
+    const bool holds = 16 * q < N;        // warps beyond the tile only rescale and store O
+    const uint32_t lane_addr = (uint32_t)(32 * q) << 16;
+    const float scale2 = a.scale * kLog2e;
+    int meets = 0;
+    auto meet = [&]() -> bool {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kMeet));
+      const bool r = wait_all(bar(kMeet), meets & 1, ctl);
+      ++meets;
+      return r;
+    };
+    uint8_t* const prow = smem + Lay::kOffP + (row < N ? row : 0) * 128;
+    PieceIter<kShared> pi(range_s.rg);
+    Piece pc;
+    int g = 0, piece = 0;
+    bool ok = true;
+    while (ok && pi.next(pc, a)) {
+      const Task k = load_task<N, kShared>(a, pc.t, grp);
+      const int n = pc.pe - pc.pa;
+      // This row sees its task's tokens t < end with t < sinks or t >= from.
+      int end = k.s.T, from = 0;
+      if (row < k.live) {
+        if (kShared && pc.t < a.tiles) {
+          const int r = k.row0 + row, b = r / a.rows;
+          end = min(k.s.T, k.s.T + a.seqlens[b] - a.s_q + 1 + (r - b * a.rows) / a.heads);
+        } else {
+          end = k.s.T - a.s_q + 1 + (k.srow + row) / a.heads;
+          if (!kShared) from = end - a.window;
+        }
+      }
+      float m = -INFINITY, l = 0.f;
+      for (int i = 0; i < n && ok; ++i) {
+        const int gs = g + i, u = gs & 1;
+        float y[32];
+        float mp = -INFINITY;
+        if (!wait_all(bar(kSFull + u), (gs >> 1) & 1, ctl)) { ok = false; break; }
+        tc_fence_after();
+        if (holds) {
+          uint32_t r[32];
+          tmem_ld16x2_32<32>(tmem + lane_addr + kColS + 64 * u, r);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) y[j] = __uint_as_float(r[j]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kSFree + u));
+        if (holds) {
+          const int t0 = k.s.real(pc.pa + i) * kPage + 32 * half;
+          uint32_t see = below(end - t0);
+          if (!kShared) see &= below(a.sinks - t0) | ~below(from - t0);
+          const uint64_t s2 = f2_pack(scale2, scale2);
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) f2_unpack(f2_mul(f2_pack(y[j], y[j + 1]), s2), y[j], y[j + 1]);
+          if (!__all_sync(0xffffffffu, see == 0xffffffffu)) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) y[j] = ((see >> j) & 1u) ? y[j] : -INFINITY;
+          }
+          float t3[10];
+#pragma unroll
+          for (int j = 0; j < 10; ++j) t3[j] = fmax3(y[3 * j], y[3 * j + 1], y[3 * j + 2]);
+          mp = fmaxf(y[30], y[31]);
+#pragma unroll
+          for (int j = 0; j < 10; j += 2) mp = fmax3(mp, t3[j], t3[j + 1]);
+          mp = fmaxf(mp, __shfl_xor_sync(0xffffffffu, mp, 16));
+        }
+        const float m_new = fmaxf(m, mp);
+        const bool need = !(m_new <= m + kRescaleThreshold);  // also while m is -inf and a token is seen
+        const float alpha = !need ? 1.f : (m == -INFINITY ? 0.f : fast_exp2(m - m_new));
+        if (need) m = m_new;
+        if (i > 0) {
+          // O^T's lanes are dims: a row's rescale concerns every warp.
+          if (half == 0) al_s[u][row] = alpha;
+          const bool any = __any_sync(0xffffffffu, need);
+          if (lane == 0) need_s[u][q] = any;
+          if (!meet()) { ok = false; break; }
+          if (need_s[u][0] | need_s[u][1] | need_s[u][2] | need_s[u][3]) {
+            if (!wait_all(bar(kODone + (u ^ 1)), ((gs - 1) >> 1) & 1, ctl)) { ok = false; break; }
+            tc_fence_after();
+#pragma unroll 1
+            for (int cc = 0; cc < 4 * N; cc += 16) {
+              uint32_t r[16];
+              tmem_ld16(tmem + lane_addr + kColO + cc, r);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * al_s[u][(cc & (N - 1)) + e]);
+              tmem_st16(tmem + lane_addr + kColO + cc, r);
+            }
+            tmem_wait_st();
+          }
+        }
+        // P of two pages ago must have been read before its buffer is rewritten.
+        if (!wait_all(bar(kODone + u), ((gs >> 1) & 1) ^ 1, ctl)) { ok = false; break; }
+        if (holds) {
+          l *= alpha;
+          const float mm = m == -INFINITY ? 0.f : m;  // a row that has seen nothing holds only masked scores
+          const uint64_t nm = f2_pack(-mm, -mm);
+          uint64_t acc0 = f2_pack(0.f, 0.f), acc1 = acc0;
+          uint32_t pk[16];
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            float a0, a1, a2, a3;
+            f2_unpack(f2_add(f2_pack(y[j], y[j + 1]), nm), a0, a1);
+            f2_unpack(f2_add(f2_pack(y[j + 2], y[j + 3]), nm), a2, a3);
+            a0 = fast_exp2(a0);
+            a1 = fast_exp2(a1);
+            a2 = fast_exp2(a2);
+            a3 = fast_exp2(a3);
+            acc0 = f2_add(acc0, f2_pack(a0, a1));
+            acc1 = f2_add(acc1, f2_pack(a2, a3));
+            pk[j / 2] = pack_bf16x2(a0, a1);
+            pk[j / 2 + 1] = pack_bf16x2(a2, a3);
+          }
+          float s0, s1, s2_, s3;
+          f2_unpack(acc0, s0, s1);
+          f2_unpack(acc1, s2_, s3);
+          l += (s0 + s1) + (s2_ + s3);
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            *reinterpret_cast<uint4*>(prow + u * Lay::kQBox + (((4 * half + c) ^ (row & 7)) * 16)) =
+                make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+        }
+        fence_proxy_async();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kPFull + u));
+      }
+      if (!ok) break;
+      // ---- epilogue: O / l in this warp's dims, lse of this warp's rows
+      const bool bad = *const_cast<volatile int*>(&bad_s[piece & 7]) != 0;
+      const int ge = g + n - 1;
+      const float l_row = l + __shfl_xor_sync(0xffffffffu, l, 16);
+      const bool none = l_row == 0.f;  // the row sees no token of the piece
+      if (!meet()) { ok = false; break; }  // every warp is done with al_s
+      if (half == 0) al_s[0][row] = bad ? NAN : (none ? 0.f : 1.f / l_row);
+      if (!meet()) { ok = false; break; }
+      if (warp == 4 && lane == 0) *const_cast<volatile int*>(&bad_s[piece & 7]) = 0;  // read by all; next used 8 pieces on
+      const bool whole = pc.pa == 0 && pc.pe == k.s.n;
+      // Rows of the partial storage (or of out) where the tile's row 0 goes.
+      size_t prow0;
+      if (whole) {
+        prow0 = kShared ? (size_t)2 * a.num_workers * N + (pc.t < a.tiles ? 0 : a.batch * a.rows) + k.row0 : k.row0;
+      } else {
+        const size_t sl = pc.t == pi.rg.b0 ? w : a.num_workers + w;
+        prow0 = (kShared ? sl : sl * a.groups + grp) * N;
+      }
+      const bool direct = whole && !kShared;
+      if (holds && half == 0 && row < k.live) {
+        const float v = bad ? NAN : (none ? -INFINITY : (m + __log2f(l_row)) * kLn2);
+        (direct ? a.lse : a.part_lse)[prow0 + row] = v;
+      }
+      if (!wait_all(bar(kODone + (ge & 1)), (ge >> 1) & 1, ctl)) { ok = false; break; }
+      tc_fence_after();
+#pragma unroll 1
+      for (int cc = 0; cc < 4 * N; cc += 16) {
+        const int r0 = cc & (N - 1), dim = 128 * (cc / N) + 32 * q + lane;
+        uint32_t r[16];
+        tmem_ld16(tmem + lane_addr + kColO + cc, r);
+        tmem_wait_ld();
+        if (direct) {
+          // Two lanes trade halves of two rows, so that each stores two dims of one.
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) {
+            const float v0 = __uint_as_float(r[e]) * al_s[0][r0 + e], v1 = __uint_as_float(r[e + 1]) * al_s[0][r0 + e + 1];
+            const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? v0 : v1, 1);
+            const int orow = r0 + e + (lane & 1);
+            if (orow < k.live)
+              *reinterpret_cast<uint32_t*>(a.out + (prow0 + orow) * kDLatent + (dim & ~1)) =
+                  lane & 1 ? pack_bf16x2(got, v1) : pack_bf16x2(v0, got);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (r0 + e < k.live) a.part_o[(prow0 + r0 + e) * kDLatent + dim] = __uint_as_float(r[e]) * al_s[0][r0 + e];
+        }
+      }
+      tc_fence_before();
+      if (!meet()) { ok = false; break; }  // al_s may be rewritten
+      if (lane == 0) mbar_arrive(bar(kOFree));
+      g += n;
+      ++piece;
+    }
+  }
+
+  // ------------------------------------------------------------ teardown
+  if (tid == 0) grid_dep_launch_dependents();  // the combine grid may launch (it waits for this grid's writes)
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------- combine
+// One warp per query row: merges the pieces of its task (window), or of its rows against
+// the prefix and against the sequence's own tokens, by their lse, in that fixed order.
+constexpr int kCombineWarps = 4;
+
+template <int N, bool kShared>
+__global__ void __launch_bounds__(kCombineWarps * 32) combine_tile_kernel(const __grid_constant__ TileArgs a) {
+  grid_dep_launch_dependents();
+  grid_dep_wait();
+  const int lane = threadIdx.x & 31;
+  const int R = a.batch * a.rows;
+  const int gr = blockIdx.x * kCombineWarps + (threadIdx.x >> 5);
+  if (gr >= R) return;
+  const int b = gr / a.rows, r = gr - b * a.rows, g = r / N, rr = r % N;
+  SeqInfo s0, s1;
+  int r0, r1;  // the row within its tile, for either task
+  if (kShared) {
+    s0 = a.task[gr / N];
+    r0 = gr % N;
+    s1 = a.task[a.tiles + b * a.groups + g];
+    r1 = rr;
+  } else {
+    s0 = a.task[b];
+    if (s0.num_pieces == 1) return;  // written by the decode grid
+    s1 = SeqInfo{0, 0, 0};
+    r0 = g * N + rr;
+    r1 = 0;
+  }
+  uint4* out4 = reinterpret_cast<uint4*>(a.out + (size_t)gr * kDLatent);  // lane: dims 8 lane .. and 256 + 8 lane ..
+  const bool bad = s0.num_pieces < 0 || s1.num_pieces < 0;
+  const int n0 = max(s0.num_pieces, 0), n = n0 + max(s1.num_pieces, 0);
+  // Storage row of piece k.
+  auto at = [&](int k) -> size_t {
+    const bool own = k >= n0;
+    const SeqInfo& s = own ? s1 : s0;
+    const int j = own ? k - n0 : k;
+    if (kShared && s.num_pieces == 1) return (size_t)2 * a.num_workers * N + (own ? R : 0) + gr;
+    const size_t slot = j == 0 ? s.first_slot : s.first_worker + j;
+    return kShared ? slot * N + (own ? r1 : r0) : slot * a.groups * N + r0;
+  };
+  const float lk = lane < n ? a.part_lse[at(lane)] : -INFINITY;
+  float L = lk;
+  bool nan = lk != lk;
+  for (int k = lane + 32; k < n; k += 32) {
+    const float v = a.part_lse[at(k)];
+    nan |= v != v;
+    L = fmaxf(L, v);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) L = fmaxf(L, __shfl_xor_sync(0xffffffffu, L, o));
+  if (bad || __any_sync(0xffffffffu, nan) || L == -INFINITY) {
+    const bool isnan = bad || __any_sync(0xffffffffu, nan);
+    const uint32_t v = isnan ? 0x7fff7fffu : 0u;
+    out4[lane] = make_uint4(v, v, v, v);
+    out4[lane + 32] = make_uint4(v, v, v, v);
+    if (lane == 0) a.lse[gr] = isnan ? NAN : -INFINITY;
+    return;
+  }
+  float acc[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+  float wsum = 0.f;
+#pragma unroll 2
+  for (int k = 0; k < n; ++k) {
+    const size_t row = at(k);
+    const float wk = expf((k < 32 ? __shfl_sync(0xffffffffu, lk, k) : a.part_lse[row]) - L);
+    wsum += wk;
+    const float4* src = reinterpret_cast<const float4*>(a.part_o + row * kDLatent);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float4 x = src[64 * h + 2 * lane], z = src[64 * h + 2 * lane + 1];
+      acc[8 * h + 0] += wk * x.x;
+      acc[8 * h + 1] += wk * x.y;
+      acc[8 * h + 2] += wk * x.z;
+      acc[8 * h + 3] += wk * x.w;
+      acc[8 * h + 4] += wk * z.x;
+      acc[8 * h + 5] += wk * z.y;
+      acc[8 * h + 6] += wk * z.z;
+      acc[8 * h + 7] += wk * z.w;
+    }
+  }
+  const float inv = 1.f / wsum;
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    out4[32 * h + lane] =
+        make_uint4(pack_bf16x2(acc[8 * h] * inv, acc[8 * h + 1] * inv), pack_bf16x2(acc[8 * h + 2] * inv, acc[8 * h + 3] * inv),
+                   pack_bf16x2(acc[8 * h + 4] * inv, acc[8 * h + 5] * inv), pack_bf16x2(acc[8 * h + 6] * inv, acc[8 * h + 7] * inv));
+  if (lane == 0) a.lse[gr] = L + logf(wsum);
+}
+
+// A launch as a programmatic dependent of the grid before it on the stream.
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), int grid, int threads, int smem, cudaStream_t stream,
+                             const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int N, bool kShared>
+cudaError_t launch_tile(const TileArgs& a, cudaStream_t stream) {
+  static bool done[64] = {};
+  cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void*>(decode_tile_kernel<N, kShared>), Layout<N>::kAlloc, done);
+  if (e != cudaSuccess) return e;
+  auto encode = tensor_map_encoder();
+  if (!encode) return cudaErrorNotSupported;
+  // The cache as [rows, 576] in boxes of 64 rows x 64 dims, q' as [rows of the batch, 576]
+  // in boxes of N rows x 64 dims; every box starts at a multiple of 64 elements.
+  CUtensorMap kv_map, q_map;
+  const cuuint32_t estr[2] = {1, 1};
+  const cuuint64_t strides[1] = {(cuuint64_t)kDQK * 2};
+  const cuuint64_t kv_rows = (cuuint64_t)(a.block_table ? a.num_pages : a.batch * a.max_blocks) * kPage;
+  const cuuint64_t kv_dims[2] = {(cuuint64_t)kDQK, kv_rows}, q_dims[2] = {(cuuint64_t)kDQK, (cuuint64_t)a.batch * a.rows};
+  const cuuint32_t kv_box[2] = {64, 64}, q_box[2] = {64, N};
+  auto map = [&](CUtensorMap* m, const __nv_bfloat16* p, const cuuint64_t* dims, const cuuint32_t* box) {
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<__nv_bfloat16*>(p), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  if (!map(&kv_map, a.kv, kv_dims, kv_box) || !map(&q_map, a.q, q_dims, q_box)) return cudaErrorInvalidValue;
+  const uint64_t limit_ns = (uint64_t)a.wait_limit * 1000000ull;
+  e = launch_dependent(decode_tile_kernel<N, kShared>, kShared ? a.num_workers : a.num_workers * a.groups, kThreads,
+                       Layout<N>::kAlloc, stream, kv_map, q_map, a, limit_ns);
+  if (e != cudaSuccess) return e;
+  const int R = a.batch * a.rows;
+  return launch_dependent(combine_tile_kernel<N, kShared>, (R + kCombineWarps - 1) / kCombineWarps, kCombineWarps * 32, 0,
+                          stream, a);
+}
+
+}  // namespace
+
+size_t plan_tile(TileArgs* a, int sm_count, int forced_workers, void* base) {
+  const bool shared = a->prefix_len != nullptr;
+  const long long R = (long long)a->batch * a->rows;
+  // The fewest tiles of at most 64 rows, then the narrowest tile that gives as few: narrow
+  // tiles leave more shared memory to the load ring.  A prefix is read by tiles of the
+  // whole batch's rows, so there the batch's rows count.
+  const long long all = shared ? R : a->rows;
+  const int tiles = (int)((all + 63) / 64), per = (int)((all + tiles - 1) / tiles);
+  a->row_tile = per <= 16 ? 16 : per <= 32 ? 32 : 64;
+  a->groups = (a->rows + a->row_tile - 1) / a->row_tile;
+  a->tiles = shared ? (int)((R + a->row_tile - 1) / a->row_tile) : 0;
+  a->num_workers = shared ? sm_count : std::max(1, sm_count / a->groups);
+  if (forced_workers > 0) a->num_workers = forced_workers;
+  const size_t tasks = shared ? (size_t)a->tiles + (size_t)a->batch * a->groups : (size_t)a->batch;
+  const size_t rows = shared ? (size_t)2 * a->num_workers * a->row_tile + 2 * (size_t)R
+                             : (size_t)2 * a->num_workers * a->groups * a->row_tile;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    char* p = base ? static_cast<char*>(base) + off : nullptr;
+    off += (bytes + 255) & ~size_t(255);
+    return p;
+  };
+  a->task = reinterpret_cast<SeqInfo*>(take(tasks * sizeof(SeqInfo)));
+  a->part_lse = reinterpret_cast<float*>(take(rows * sizeof(float)));
+  a->part_o = reinterpret_cast<float*>(take(rows * kDLatent * sizeof(float)));
+  return off;
+}
+
+void tile_schedule(TileArgs* a) {
+  const int mp = knob_value(MLA_KNOB_MIN_PAGES), pc = knob_value(MLA_KNOB_PIECE_COST);
+  const int policy = knob_value(MLA_KNOB_SPLIT_POLICY);
+  a->min_pages = mp > 0 ? mp : 2;
+  a->piece_cost = pc > 0 ? std::min(pc - 1, kMaxPieceCost) : 3;
+  a->whole_slack = knob_value(MLA_KNOB_NUM_WORKERS) > 0 || policy == 1 ? -1 : policy == 2 ? 1 << 30 : 2;
+}
+
+cudaError_t launch_decode_tile(const TileArgs& a, cudaStream_t stream) {
+  if (a.prefix_len)
+    return a.row_tile == 16   ? launch_tile<16, true>(a, stream)
+           : a.row_tile == 32 ? launch_tile<32, true>(a, stream)
+                              : launch_tile<64, true>(a, stream);
+  return a.row_tile == 16   ? launch_tile<16, false>(a, stream)
+         : a.row_tile == 32 ? launch_tile<32, false>(a, stream)
+                            : launch_tile<64, false>(a, stream);
+}
+
+}  // namespace mla

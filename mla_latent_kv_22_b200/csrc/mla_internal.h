@@ -104,6 +104,68 @@ int decode_pair_max_workers(int sm_count);
 cudaError_t launch_decode(int kernel, const DecodeArgs& a, cudaStream_t stream);
 int decode_granule(int kernel);
 
+// Sliding-window and shared-prefix decode (decode_tile.cu): one CTA per worker, query
+// rows in tiles of row_tile (16, 32 or 64).  The schedule's entries ("tasks") are, for a
+// window, the sequences (worker w of group g walks the pages for rows [g row_tile, +) of
+// each sequence, so the `groups` CTAs of one worker read the same pages side by side);
+// for a shared prefix, first the prefix once for each of the `tiles` row tiles of the
+// whole batch, then each sequence's own tokens once for each of its groups.
+struct TileArgs {
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* kv;
+  const int32_t* block_table;  // null = contiguous cache (window only)
+  const int32_t* seqlens;
+  const int32_t* prefix_table;  // shared prefix only
+  const int32_t* prefix_len;    // device, one value; null = window
+  __nv_bfloat16* out;
+  float* lse;
+  int batch, s_q, heads, rows;  // rows = s_q x heads query rows per sequence
+  int num_pages, max_blocks, prefix_blocks;
+  int window, sinks;
+  float scale;
+  int* err;
+  int row_tile, groups, tiles;
+  // Workspace: a record per task; split partials [2 workers][groups (window) or 1][row_tile]
+  // and, for a shared prefix, the unsplit results of all rows against the prefix and
+  // against their own tokens.
+  SeqInfo* task;
+  float* part_lse;
+  float* part_o;
+  int num_workers;
+  int min_pages, whole_slack, piece_cost;
+  int wait_limit, withhold_arrive;
+};
+
+// Fills row_tile, groups, tiles, num_workers and the workspace pointers for the sizes
+// already in `a`; returns the workspace bytes (`base` may be null to compute the size).
+// forced_workers > 0 sets the number of workers.
+size_t plan_tile(TileArgs* a, int sm_count, int forced_workers, void* base);
+// Sets the schedule's constants for the current knobs.
+void tile_schedule(TileArgs* a);
+cudaError_t launch_decode_tile(const TileArgs& a, cudaStream_t stream);
+
+// Cache append with position rotation (append.cu).
+struct AppendArgs {
+  const __nv_bfloat16* c_kv;
+  const __nv_bfloat16* k_rope;
+  const __nv_bfloat16* q_rope;  // null = no query part
+  __nv_bfloat16* q_out;
+  const float* cos_sin;
+  const int32_t* cu_tokens;  // null = tokens / batch tokens per sequence
+  const int32_t* seqlens;
+  const int32_t* pos_offset;  // null = 0
+  const int32_t* block_table;  // null = contiguous cache
+  __nv_bfloat16* kv;
+  long long ckv_stride, krope_stride, q_stride_n, q_stride_h, qo_stride_n, qo_stride_h;  // elements
+  int tokens, batch, heads, num_pages, max_blocks, max_pos;
+  int* err;
+};
+cudaError_t launch_append(const AppendArgs& a, bool interleaved, cudaStream_t stream);
+
+// Value absorption of a bf16 latent (absorb.cu).
+cudaError_t launch_absorb_o_bf16(const __nv_bfloat16* out_latent, const __nv_bfloat16* w_uv, float* out, int batch,
+                                 int heads, int* err, cudaStream_t stream);
+
 // cuTensorMapEncodeTiled from the driver (resolved once; null if unavailable).  Defined in api.cu.
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 

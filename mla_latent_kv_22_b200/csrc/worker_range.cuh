@@ -36,14 +36,27 @@ struct RangeScratch {
   WorkerRange rg;
 };
 
+// The lengths a schedule is made of, for a batch of plain sequences: pages(b) is the
+// page count of sequence b (0 when its length is invalid), bad(b) whether it is invalid.
+struct SeqLengths {
+  const int32_t* seqlens;
+  int max_blocks;
+  __device__ __forceinline__ int pages(int b) const { return seq_pages(seqlens, max_blocks, b); }
+  __device__ __forceinline__ bool bad(int b) const {
+    const int T = seqlens[b];
+    return T < 0 || T > max_blocks * kPage;
+  }
+};
+
 // Called by every thread of the CTA (block-uniform control flow, blockDim.x a multiple
-// of 32) with the call's lengths, batch size B, block-table width, worker count P and
-// schedule knobs; writes this CTA's share of the records `seq`, and on return rs.rg
-// holds worker w's range (b0 < 0: no work).  Not inlined: it runs once per CTA and
-// keeps its registers out of the kernel's main loops.
-static __device__ __noinline__ void derive_worker_range(const int32_t* seqlens, int B, int max_blocks, int P,
-                                                       int min_pages, int granule, int whole_slack, int piece_cost,
-                                                       SeqInfo* seq, int* err, int w, RangeScratch& rs) {
+// of 32) with the call's lengths, their number B, worker count P and schedule knobs;
+// writes this CTA's share of the records `seq`, and on return rs.rg holds worker w's
+// range (b0 < 0: no work).  Not inlined: it runs once per CTA and keeps its registers
+// out of the kernel's main loops.
+template <class Lengths>
+static __device__ __noinline__ void derive_range(const Lengths len, int B, int P, int min_pages, int granule,
+                                                 int whole_slack, int piece_cost, SeqInfo* seq, int* err, int w,
+                                                 RangeScratch& rs) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
   auto owns = [&](int b) { return b % (int)gridDim.x == (int)blockIdx.x; };
   auto units = [&](int n) { return n > 0 ? n + piece_cost : 0; };  // a sequence's share of the layout
@@ -52,7 +65,7 @@ static __device__ __noinline__ void derive_worker_range(const int32_t* seqlens, 
   long long sum = 0, wsum = 0;
   int mx = 0;
   for (int b = tid; b < B; b += blockDim.x) {
-    const int n = seq_pages(seqlens, max_blocks, b);
+    const int n = len.pages(b);
     sum += n;
     wsum += units(n);
     mx = max(mx, n);
@@ -95,15 +108,14 @@ static __device__ __noinline__ void derive_worker_range(const int32_t* seqlens, 
   if (whole_slack >= 0 && B <= P && rs.maxp <= share(rs.total) + whole_slack) {
     // 2a. One whole sequence per worker.
     if (tid == 0 && w < B) {
-      const int n = seq_pages(seqlens, max_blocks, w);
+      const int n = len.pages(w);
       if (n > 0) rs.rg = WorkerRange{w, 0, w, n};
     }
     for (int b = tid; b < B; b += blockDim.x) {
       if (!owns(b)) continue;
-      const int T = seqlens[b];
-      const bool bad = T < 0 || T > max_blocks * kPage;
+      const bool bad = len.bad(b);
       if (bad) set_device_error(err, MLA_ERR_DEVICE_BAD_PAGE);
-      seq[b] = SeqInfo{b, bad ? -1 : (T > 0 ? 1 : 0), b};
+      seq[b] = SeqInfo{b, bad ? -1 : (len.pages(b) > 0 ? 1 : 0), b};
     }
     __syncthreads();
     return;
@@ -120,7 +132,7 @@ static __device__ __noinline__ void derive_worker_range(const int32_t* seqlens, 
   const long long g0 = (long long)w * q, g1 = min(g0 + q, (long long)W);
   for (int base = 0; base < B; base += blockDim.x) {
     const int b = base + tid;
-    const int n = b < B ? seq_pages(seqlens, max_blocks, b) : 0;
+    const int n = b < B ? len.pages(b) : 0;
     const int u = units(n);
     int x = u;
 #pragma unroll
@@ -146,8 +158,7 @@ static __device__ __noinline__ void derive_worker_range(const int32_t* seqlens, 
         }
       }
       if (owns(b)) {
-        const int T = seqlens[b];
-        const bool bad = T < 0 || T > max_blocks * kPage;
+        const bool bad = len.bad(b);
         if (bad) set_device_error(err, MLA_ERR_DEVICE_BAD_PAGE);
         SeqInfo si;
         si.first_worker = pos / q;
@@ -163,6 +174,13 @@ static __device__ __noinline__ void derive_worker_range(const int32_t* seqlens, 
     if (tid == blockDim.x - 1) rs.carry = st + u;
     __syncthreads();
   }
+}
+
+// The schedule of a batch of plain sequences.
+static __device__ __forceinline__ void derive_worker_range(const int32_t* seqlens, int B, int max_blocks, int P,
+                                                           int min_pages, int granule, int whole_slack, int piece_cost,
+                                                           SeqInfo* seq, int* err, int w, RangeScratch& rs) {
+  derive_range(SeqLengths{seqlens, max_blocks}, B, P, min_pages, granule, whole_slack, piece_cost, seq, err, w, rs);
 }
 
 }  // namespace mla

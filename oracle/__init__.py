@@ -41,3 +41,9 @@ from .mla_oracle import (  # noqa: F401
     latent_cache_bytes,
 )
 from .fp8_cache import e4m3_to_f64, dequant_rows, mla_decode_fp8_ref  # noqa: F401
+from .serving import (  # noqa: F401
+    mla_decode_window_ref,
+    mla_decode_shared_ref,
+    mla_append_ref,
+    rotate_ref,
+)
