@@ -14,13 +14,16 @@
 // tensor-parallel shard) run at the speed of the loads, and the rows of many sequences are
 // packed into tiles of 64 where they share the tokens (a common prefix).
 //
-// Roles (256 threads).  Warp 0: page loads (TMA) into two rings, one of 16 KB slots (128
-// latent dims of a page, four per page; freed by the second product) and one of 8 KB slots
-// (the rope dims, freed by the first).  Warp 1: tensor memory and MMA issue.  Warp 2:
-// zeroes the rows of a page that no query of the sequence sees (past its end, or between
-// the sinks and the window), where a masked P of 0 would meet whatever the cache holds.
-// Warp 3: q' loads, one tile per piece.  Warps 4-7: softmax of the 16 rows in their TMEM
-// quadrant (two threads per row, 32 tokens each) and the epilogue.
+// Roles (256 threads).  Warp 0: page loads (TMA), two 32 KB halves of 256 latent dims per
+// page into a ring, freed by the second product, and the rope dims into two 8 KB slots,
+// freed by the first.  Warp 1: q' loads and the first product's MMAs.  Warp 2: zeroes the
+// rows of a page that no query of the sequence sees (past its end, or between the sinks
+// and the window), where a masked P of 0 would meet whatever the cache holds.  Warp 3:
+// tensor memory and the second product's MMAs.  (One warp issuing both products was bound
+// by its own instruction stream: 52 MMAs of ~35 cycles and 14 waits and commits of
+// 70-110 a page; two warps, and one commit per half, overlap them.)  Warps 4-7: softmax
+// of the 16 rows in their TMEM quadrant (two threads per row, 32 tokens each) and the
+// epilogue.
 //
 // The running maximum is lazy as in decode_pair.cu: O and the sum are rescaled only when a
 // page's maximum exceeds the reference by more than 2^8.  Since O's lanes are dims, all
@@ -47,50 +50,49 @@ using namespace sm100;
 
 constexpr int kThreads = 256;
 constexpr int kBox = 8192;            // [64 tokens x 64 bf16], 128B swizzle
-constexpr int kSlotBytes = 2 * kBox;  // a latent slot: 128 dims of a page
-constexpr int kPageSlots = 4;
+constexpr int kSlotBytes = 4 * kBox;  // a ring slot: one half (256 latent dims) of a page
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 0, kColS = 256;  // O^T: block m at 4 columns-of-N m; S: two buffers of 64 columns
 
-// Shared memory for a row tile of N: q' (9 boxes of [N rows x 64 dims]), P (two buffers of
-// [N rows x 64 tokens]), the rope ring and the latent ring.
+// Shared memory for a row tile of N: q' (9 boxes of [N rows x 64 dims]; twice where the
+// ring keeps its five slots, so that a piece's q' loads under the one before), P ([N rows
+// x 64 tokens], two buffers where they fit), two rope slots and the latent ring.
 template <int N>
 struct Layout {
   static constexpr int kQBox = N * 128;
-  static constexpr int kRopeSlots = N == 64 ? 1 : 3;
-  static constexpr int kSlots = N == 64 ? 8 : N == 32 ? 9 : 11;
+  static constexpr int kQBufs = N == 16 ? 2 : 1;
+  static constexpr int kPBufs = N == 64 ? 1 : 2;
+  static constexpr int kSlots = N == 64 ? 4 : 5;
   static constexpr int kOffQ = 0;
-  static constexpr int kOffP = 9 * kQBox;
-  static constexpr int kOffRope = kOffP + 2 * kQBox;
-  static constexpr int kOffRing = kOffRope + kRopeSlots * kBox;
+  static constexpr int kOffP = kQBufs * 9 * kQBox;
+  static constexpr int kOffRope = kOffP + kPBufs * kQBox;
+  static constexpr int kOffRing = kOffRope + 2 * kBox;
   static constexpr int kBytes = kOffRing + kSlots * kSlotBytes;
   static constexpr int kAlloc = kBytes + 1024;  // + alignment slack
   static_assert(N == 16 || N == 32 || N == 64, "row tile");
   // The first product reads 64 rows of every q' box; the last box's reach stays inside.
-  static_assert(8 * kQBox + 64 * 128 <= kBytes, "q' rows read outside the allocation");
+  static_assert((kQBufs * 9 - 1) * kQBox + 64 * 128 <= kBytes, "q' rows read outside the allocation");
   static_assert(kQBox % 1024 == 0 && kOffRope % 1024 == 0 && kOffRing % 1024 == 0, "1024-byte tiles");
   static_assert(kAlloc + 2048 <= 232448, "dynamic + static shared memory above the per-CTA limit");
   static_assert(4 * N <= 256 && kColS + 128 <= kTmemCols, "tensor-memory regions overlap");
 };
-constexpr int kMaxSlots = 11, kMaxRope = 3;
+constexpr int kMaxSlots = 5;
 
 enum Bar {
-  kFull = 0,                     // [slot] a latent slot landed (and, if dirty, was cleaned)
-  kEmpty = kFull + kMaxSlots,    // [slot] the second product has read it
-  kDirty = kEmpty + kMaxSlots,   // [slot] a latent slot with unseen rows landed
-  kRFull = kDirty + kMaxSlots,   // [rope slot]
-  kREmpty = kRFull + kMaxRope,   // [rope slot]
-  kQFull = kREmpty + kMaxRope,
-  kQEmpty,                       // the piece's last first product has read q'
-  kSFull,                        // [2] scores of a page are in S
-  kSFree = kSFull + 2,           // [2] the 4 softmax warps have read them
-  kPFull = kSFree + 2,           // [2] the 4 softmax warps wrote P (and rescaled O)
-  kODone = kPFull + 2,           // [2] the second product of a page is done
-  kOFree = kODone + 2,           // the 4 softmax warps read O in the epilogue
-  kMeet,                         // the 4 softmax warps met
-  kDrain,
-  kNumBars
+  kFull = 0,                   // [slot] a half landed (and, if dirty, was cleaned)
+  kEmpty = kFull + kMaxSlots,  // [slot] the second product has read it
+  kDirty = kEmpty + kMaxSlots, // [slot] a half with unseen rows landed
+  kQFull = kDirty + kMaxSlots, // [2] q' of a piece landed
+  kQEmpty = kQFull + 2,        // [2] the piece's last first product has read q'
+  kSFull = kQEmpty + 2,        // [2] scores of a page are in S (and its rope slot is free)
+  kSFree = kSFull + 2,         // [2] the 4 softmax warps have read them
+  kPFull = kSFree + 2,         // [2] the 4 softmax warps wrote P (and rescaled O)
+  kODone = kPFull + 2,         // [2] the second product of a page is done
+  kOFree = kODone + 2,         // the 4 softmax warps read O in the epilogue
+  kMeet,                       // the 4 softmax warps met
+  kDrain,                      // [2] either issuing warp's MMAs are all done
+  kNumBars = kDrain + 2
 };
 
 __device__ __forceinline__ uint64_t now_ns() {
@@ -248,10 +250,11 @@ __device__ __forceinline__ uint32_t below(int x) { return x <= 0 ? 0u : x >= 32 
 
 template <int N, bool kShared>
 __global__ void __launch_bounds__(kThreads, 1)
-    decode_tile_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap q_map,
+    decode_tile_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap rope_map,
+                       const __grid_constant__ CUtensorMap q_map,
                        const __grid_constant__ TileArgs a, uint64_t limit_ns) {
   using Lay = Layout<N>;
-  constexpr int kSlots = Lay::kSlots, kRope = Lay::kRopeSlots;
+  constexpr int kSlots = Lay::kSlots;
   constexpr uint32_t kIdescS = idesc_bf16_f32(64, 64, 0, 0);   // A q' K-major, B rows K-major
   constexpr uint32_t kIdescO = idesc_bf16_f32(128, N, 1, 0);   // A rows MN-major, B P K-major
   extern __shared__ uint8_t smem_raw[];
@@ -279,13 +282,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(kEmpty + s), 1);  // MMA commit
       mbar_init(bar(kDirty + s), 1);
     }
-    for (int s = 0; s < kRope; ++s) {
-      mbar_init(bar(kRFull + s), 1);
-      mbar_init(bar(kREmpty + s), 1);
-    }
-    mbar_init(bar(kQFull), 1);
-    mbar_init(bar(kQEmpty), 1);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(kQFull + i), 1);
+      mbar_init(bar(kQEmpty + i), 1);
+      mbar_init(bar(kDrain + i), 1);
       mbar_init(bar(kSFull + i), 1);
       mbar_init(bar(kSFree + i), 4);
       mbar_init(bar(kPFull + i), 4);
@@ -293,12 +293,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(bar(kOFree), 4);
     mbar_init(bar(kMeet), 4);
-    mbar_init(bar(kDrain), 1);
     fence_mbar_init();
     tma_prefetch_desc(&kv_map);
+    tma_prefetch_desc(&rope_map);
     tma_prefetch_desc(&q_map);
   }
-  if (warp == 1) {
+  if (warp == 3) {
     tmem_alloc(smem_u32(&tmem_base_s), kTmemCols);
     tmem_relinquish();
   }
@@ -317,17 +317,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ page loads
     PieceIter<kShared> pi(range_s.rg);
     Piece pc;
-    int slot = 0, rslot = 0, piece = 0, fills = 0;
-    uint32_t phase = 1, rphase = 1;       // parity of the "empty" phase to wait for
-    uint32_t dpar = 0;                    // [slot] parity of the slot's next dirty fill
-    uint32_t was_dirty = 0, was = 0;      // [slot] the last fill was dirty; there was one
-    uint32_t lpar = 0, rpar = 0, rwas = 0;  // [slot] parity of the last fill's "full" phase
+    int slot = 0, piece = 0, fills = 0, g = 0;
+    uint32_t phase = 1;               // parity of the "empty" phase to wait for
+    uint32_t dpar = 0;                // [slot] parity of the slot's next dirty fill
+    uint32_t was_dirty = 0, was = 0;  // [slot] the last fill was dirty; there was one
+    uint32_t lpar = 0;                // [slot] parity of the last fill's phase
     int withheld = -1;
     bool ok = true;
     while (ok && pi.next(pc, a)) {
       const Task k = load_task<N, kShared>(a, pc.t, grp);
       int ids = 0, ids_at = pc.pa - 32;  // lane l holds the id of list page ids_at + l
-      for (int p = pc.pa; p < pc.pe && ok; ++p) {
+      for (int p = pc.pa; p < pc.pe && ok; ++p, ++g) {
         if (p >= ids_at + 32) {
           ids_at = p;
           const int pp = p + lane;
@@ -342,19 +342,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int y = (unsigned)id < (unsigned)np ? id * kPage : np * kPage;  // out of range: reads zeros
         const bool dirty = page_dirty(k.s, k.s.real(p));
 #pragma unroll 1
-        for (int m = 0; m < kPageSlots; ++m) {
-          if (!wait_all(bar(kEmpty + slot), phase, ctl)) { ok = false; break; }
+        for (int m = 0; m < 2; ++m) {
+          // The page's rope rides on its second half; its slot is free once the scores of
+          // two pages ago are done.
+          if (!wait_all(bar(kEmpty + slot), phase, ctl) ||
+              (m == 1 && !wait_all(bar(kSFull + (g & 1)), ((g >> 1) & 1) ^ 1, ctl))) {
+            ok = false;
+            break;
+          }
           const uint32_t bit = 1u << slot;
-          if (lane == 0) {
+          if (a.withhold_arrive && blockIdx.x == 0 && fills == 1) {
+            withheld = slot;  // timeout test: this fill never completes
+          } else if (lane == 0) {
             const uint32_t b = bar((dirty ? kDirty : kFull) + slot);
-            if (a.withhold_arrive && blockIdx.x == 0 && fills == 1) {
-              withheld = slot;  // timeout test: this fill never completes
-            } else {
-              const uint32_t dst = sbase + Lay::kOffRing + slot * kSlotBytes;
-              mbar_expect_tx(b, kSlotBytes);
-              tma_load_2d(dst, &kv_map, 128 * m, y, b);
-              tma_load_2d(dst + kBox, &kv_map, 128 * m + 64, y, b);
-            }
+            mbar_expect_tx(b, kSlotBytes + (m == 1 ? kBox : 0));
+            tma_load_3d(sbase + Lay::kOffRing + slot * kSlotBytes, &kv_map, 0, y, 4 * m, b);
+            if (m == 1) tma_load_3d(sbase + Lay::kOffRope + (g & 1) * kBox, &rope_map, 0, y, 8, b);
           }
           if (dirty) {
             lpar = (lpar & ~bit) | (dpar & bit);
@@ -371,17 +374,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             phase ^= 1u;
           }
         }
-        if (!ok || !wait_all(bar(kREmpty + rslot), rphase, ctl)) { ok = false; break; }
-        if (lane == 0) {
-          mbar_expect_tx(bar(kRFull + rslot), kBox);
-          tma_load_2d(sbase + Lay::kOffRope + rslot * kBox, &kv_map, kDLatent, y, bar(kRFull + rslot));
-        }
-        rwas |= 1u << rslot;
-        rpar = (rpar & ~(1u << rslot)) | ((rphase ^ 1u) << rslot);
-        if (++rslot == kRope) {
-          rslot = 0;
-          rphase ^= 1u;
-        }
       }
       ++piece;
     }
@@ -390,113 +382,73 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int s = 0; s < kSlots; ++s)
         if (((was >> s) & 1u) && s != withheld)
           drain_wait(bar((((was_dirty >> s) & 1u) ? kDirty : kFull) + s), (lpar >> s) & 1u, limit_ns);
-      for (int s = 0; s < kRope; ++s)
-        if ((rwas >> s) & 1u) drain_wait(bar(kRFull + s), (rpar >> s) & 1u, limit_ns);
     }
     __syncwarp();
   } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issue
-    PieceIter<kShared> pi(range_s.rg);
-    Piece pc;
-    // Descriptors: a K-major step of 16 dims is 32 bytes, an MN-major step of 16 tokens
-    // 2048 bytes; the two 64-dim boxes of a slot are the MN-major halves of 128 dims.
-    constexpr uint64_t kKMajor = desc_sw128_const(16, 1024), kMNMajor = desc_sw128_const(kBox, 1024);
-    const uint64_t dq = kKMajor | desc_addr(sbase + Lay::kOffQ);
-    const uint64_t dp = kKMajor | desc_addr(sbase + Lay::kOffP);
+    // ------------------------------------------------------------ q' loads, scores
+    PieceIter<kShared> pi(range_s.rg), pq(range_s.rg);  // pq: the next piece whose q' is loaded
+    Piece pc, qc;
+    // Descriptors: a K-major step of 16 dims is 32 bytes.
+    constexpr uint64_t kKMajor = desc_sw128_const(16, 1024);
+    const uint64_t dq0 = kKMajor | desc_addr(sbase + Lay::kOffQ);
     const uint64_t drope = kKMajor | desc_addr(sbase + Lay::kOffRope);
     const uint32_t ring = desc_addr(sbase + Lay::kOffRing);
-    int slot = 0, vslot = 0, rslot = 0, piece = 0;  // next slot of the first / second product
-    uint32_t phase = 0, rphase = 0;
-    int g = 0;
-    bool ok = true;
-    // Scores of page gs into S buffer gs & 1.
-    auto do_s = [&](int gs) -> bool {
-      if (!wait_all(bar(kSFree + (gs & 1)), ((gs >> 1) & 1) ^ 1, ctl)) return false;
-      tc_fence_after();
-      const uint32_t d = tmem + kColS + 64 * (gs & 1);
-#pragma unroll 1
-      for (int m = 0; m < kPageSlots; ++m) {
-        if (!wait_all(bar(kFull + slot), phase, ctl)) return false;
-        tc_fence_after();
-        const uint64_t bk = kKMajor | (ring + slot * (kSlotBytes >> 4));
-        mma_x4_elect<2, 2>(d, dq + (2 * m) * (Lay::kQBox >> 4), bk, kIdescS, m ? 1u : 0u);
-        mma_x4_elect<2, 2>(d, dq + (2 * m + 1) * (Lay::kQBox >> 4), bk + (kBox >> 4), kIdescS, 1u);
-        if (++slot == kSlots) {
-          slot = 0;
-          phase ^= 1u;
-        }
+    constexpr int kQBufs = Lay::kQBufs;
+    int slot = 0, piece = 0, loaded = 0, g = 0;
+    uint32_t phase = 0;
+    bool ok = true, more = true;
+    // q' of the next piece into its buffer, once the piece that used it is done with it.
+    auto load_q = [&]() -> bool {
+      if (!more || !(more = pq.next(qc, a))) return true;
+      const int qb = loaded % kQBufs;
+      if (!wait_all(bar(kQEmpty + qb), ((loaded / kQBufs) & 1) ^ 1, ctl)) return false;
+      if (lane == 0) {
+        mbar_expect_tx(bar(kQFull + qb), 9 * Lay::kQBox);
+        tma_load_3d(sbase + Lay::kOffQ + qb * 9 * Lay::kQBox, &q_map, 0, load_task<N, kShared>(a, qc.t, grp).row0, 0,
+                    bar(kQFull + qb));
       }
-      if (!wait_all(bar(kRFull + rslot), rphase, ctl)) return false;
-      tc_fence_after();
-      mma_x4_elect<2, 2>(d, dq + 8 * (Lay::kQBox >> 4), drope + rslot * (kBox >> 4), kIdescS, 1u);
-      mma_commit_elect(bar(kREmpty + rslot));
-      mma_commit_elect(bar(kSFull + (gs & 1)));
-      if (++rslot == kRope) {
-        rslot = 0;
-        rphase ^= 1u;
-      }
+      ++loaded;
+      __syncwarp();
       return true;
     };
-    auto do_o = [&](int gs, bool first) -> bool {
-      if (!wait_all(bar(kPFull + (gs & 1)), (gs >> 1) & 1, ctl)) return false;
-      if (first && piece > 0 && !wait_all(bar(kOFree), (piece - 1) & 1, ctl)) return false;
-      tc_fence_after();
-      const uint64_t bp = dp + (uint64_t)((gs & 1) * (Lay::kQBox >> 4));
-#pragma unroll 1
-      for (int m = 0; m < kPageSlots; ++m) {
-        const uint64_t av = kMNMajor | (ring + vslot * (kSlotBytes >> 4));
-        mma_x4_elect<128, 2>(tmem + kColO + N * m, av, bp, kIdescO, first ? 0u : 1u);
-        mma_commit_elect(bar(kEmpty + vslot));
-        if (++vslot == kSlots) vslot = 0;
-      }
-      mma_commit_elect(bar(kODone + (gs & 1)));
-      return true;
-    };
+    ok = load_q();
     while (ok && pi.next(pc, a)) {
       const int n = pc.pe - pc.pa;
-      if (!wait_all(bar(kQFull), piece & 1, ctl)) { ok = false; break; }
-      tc_fence_after();
-      for (int i = 0; i <= n && ok; ++i) {
-        bool o_done = i == 0;
-        if (i < n) {
-          // The second product of page i - 1 goes first when its P is ready before the last
-          // slot of page i: it frees the slots that further loads wait for.
-          if (i > 0) {
-            int s3 = slot + 3;
-            uint32_t p3 = phase;
-            if (s3 >= kSlots) {
-              s3 -= kSlots;
-              p3 ^= 1u;
-            }
-            const int gp = g + i - 1;
-            const uint32_t pbar = bar(kPFull + (gp & 1)), fbar = bar(kFull + s3);
-            uint64_t t0 = 0;
-            for (uint32_t it = 1;; ++it) {
-              if (__all_sync(0xffffffffu, mbar_test(pbar, (gp >> 1) & 1))) {
-                ok = do_o(gp, i == 1);
-                o_done = true;
-                break;
-              }
-              if (__all_sync(0xffffffffu, mbar_test(fbar, p3))) break;
-              if ((it & 63) == 0) {
-                const uint64_t t = now_ns();
-                if (t0 == 0) t0 = t;
-                // Past the limit, or aborted: the bounded wait that follows says so.
-                if (__any_sync(0xffffffffu, *ctl.abort || t - t0 > limit_ns)) break;
-              }
-            }
+      const int qb = piece % kQBufs;
+      if (!wait_all(bar(kQFull + qb), (piece / kQBufs) & 1, ctl)) { ok = false; break; }
+      const uint64_t dq = dq0 + (uint64_t)(qb * (9 * Lay::kQBox >> 4));
+      for (int i = 0; i < n && ok; ++i, ++g) {
+        if (!wait_all(bar(kSFree + (g & 1)), ((g >> 1) & 1) ^ 1, ctl)) { ok = false; break; }
+        const uint32_t d = tmem + kColS + 64 * (g & 1);
+#pragma unroll 1
+        for (int m = 0; m < 2; ++m) {
+          if (!wait_all(bar(kFull + slot), phase, ctl)) { ok = false; break; }
+          tc_fence_after();
+          const uint64_t bk = kKMajor | (ring + slot * (kSlotBytes >> 4));
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            mma_x4_elect<2, 2>(d, dq + (uint64_t)((4 * m + j) * (Lay::kQBox >> 4)), bk + (uint64_t)(j * (kBox >> 4)), kIdescS,
+                               m + j ? 1u : 0u);
+          if (++slot == kSlots) {
+            slot = 0;
+            phase ^= 1u;
           }
-          if (ok) ok = do_s(g + i);
-          if (ok && i == n - 1) mma_commit_elect(bar(kQEmpty));
         }
-        if (ok && !o_done) ok = do_o(g + i - 1, i == 1);
+        if (!ok) break;
+        mma_x4_elect<2, 2>(d, dq + 8 * (Lay::kQBox >> 4), drope + (g & 1) * (kBox >> 4), kIdescS, 1u);
+        mma_commit_elect(bar(kSFull + (g & 1)));
+        if (kQBufs == 2 && i == 0) ok = load_q();
       }
-      g += n;
+      if (!ok) break;
+      mma_commit_elect(bar(kQEmpty + qb));
+      if (kQBufs == 1) ok = load_q();
       ++piece;
     }
-    // Every MMA issued is done before tensor memory is released (bounded).
+    // The MMAs issued are done before tensor memory is released, q' has landed (bounded).
     mma_commit_elect(bar(kDrain));
     drain_wait(bar(kDrain), 0, limit_ns);
+    for (int j = 1; j <= kQBufs && j <= loaded; ++j)
+      drain_wait(bar(kQFull + (loaded - j) % kQBufs), ((loaded - j) / kQBufs) & 1, limit_ns);
     __syncwarp();
   } else if (warp == 2) {
     // ------------------------------------------------------------ rows in no query's sight
@@ -510,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int p = pc.pa; p < pc.pe && ok; ++p) {
         const int real = k.s.real(p), t0 = real * kPage;
         if (!page_dirty(k.s, real)) {
-          slot += kPageSlots;
+          slot += 2;
           if (slot >= kSlots) slot -= kSlots;
           continue;
         }
@@ -518,14 +470,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int h0 = max(k.s.hole0 - t0, 0), h1 = max(h0, min(k.s.hole1 - t0, kPage));
         const int e0 = min(max(k.s.T - t0, 0), kPage);
         const int nrow = (h1 - h0) + (kPage - e0);
-        for (int m = 0; m < kPageSlots; ++m) {
+        for (int m = 0; m < 2; ++m) {
           if (!wait_all(bar(kDirty + slot), (dpar >> slot) & 1u, ctl)) { ok = false; break; }
           dpar ^= 1u << slot;
           uint8_t* st = smem + Lay::kOffRing + slot * kSlotBytes;
-          for (int idx = lane; idx < 2 * nrow * 8; idx += 32) {
-            const int box = idx / (nrow * 8), rem = idx % (nrow * 8);
-            const int r = rem / 8, row = r < h1 - h0 ? h0 + r : e0 + (r - (h1 - h0));
-            *reinterpret_cast<uint4*>(st + box * kBox + row * 128 + (rem % 8) * 16) = make_uint4(0, 0, 0, 0);
+          for (int idx = lane; idx < nrow * 8; idx += 32) {
+            const int r = idx / 8, row = r < h1 - h0 ? h0 + r : e0 + (r - (h1 - h0));
+#pragma unroll
+            for (int box = 0; box < 4; ++box)
+              *reinterpret_cast<uint4*>(st + box * kBox + row * 128 + (idx % 8) * 16) = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async();
           __syncwarp();
@@ -535,21 +488,40 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 3) {
-    // ------------------------------------------------------------ q' of each piece
-    if (lane == 0) {
-      PieceIter<kShared> pi(range_s.rg);
-      Piece pc;
-      int piece = 0;
-      while (pi.next(pc, a)) {
-        const Task k = load_task<N, kShared>(a, pc.t, grp);
-        if (!wait_bar(bar(kQEmpty), (piece & 1) ^ 1, ctl)) break;
-        mbar_expect_tx(bar(kQFull), 9 * Lay::kQBox);
-        for (int d = 0; d < 9; ++d)
-          tma_load_2d(sbase + Lay::kOffQ + d * Lay::kQBox, &q_map, 64 * d, k.row0, bar(kQFull));
-        ++piece;
+    // ------------------------------------------------------------ O^T += V^T P^T
+    // An MN-major step of 16 tokens is 2048 bytes; two 64-dim boxes side by side are the
+    // MN-major halves of 128 dims.
+    PieceIter<kShared> pi(range_s.rg);
+    Piece pc;
+    constexpr uint64_t kKMajor = desc_sw128_const(16, 1024), kMNMajor = desc_sw128_const(kBox, 1024);
+    const uint64_t dp = kKMajor | desc_addr(sbase + Lay::kOffP);
+    const uint32_t ring = desc_addr(sbase + Lay::kOffRing);
+    int slot = 0, piece = 0, g = 0;
+    bool ok = true;
+    while (ok && pi.next(pc, a)) {
+      const int n = pc.pe - pc.pa;
+      for (int i = 0; i < n; ++i, ++g) {
+        if (!wait_all(bar(kPFull + (g & 1)), (g >> 1) & 1, ctl) ||
+            (i == 0 && piece > 0 && !wait_all(bar(kOFree), (piece - 1) & 1, ctl))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint64_t bp = dp + (uint64_t)((g % Lay::kPBufs) * (Lay::kQBox >> 4));
+#pragma unroll 1
+        for (int m = 0; m < 2; ++m) {
+          const uint64_t av = kMNMajor | (ring + slot * (kSlotBytes >> 4));
+          mma_x4_elect<128, 2>(tmem + kColO + N * 2 * m, av, bp, kIdescO, i ? 1u : 0u);
+          mma_x4_elect<128, 2>(tmem + kColO + N * (2 * m + 1), av + 2 * (kBox >> 4), bp, kIdescO, i ? 1u : 0u);
+          mma_commit_elect(bar(kEmpty + slot));
+          if (++slot == kSlots) slot = 0;
+        }
+        mma_commit_elect(bar(kODone + (g & 1)));
       }
-      if (piece > 0) drain_wait(bar(kQFull), (piece - 1) & 1, limit_ns);
+      ++piece;
     }
+    mma_commit_elect(bar(kDrain + 1));
+    drain_wait(bar(kDrain + 1), 0, limit_ns);
     __syncwarp();
   } else {
     // ------------------------------------------------------------ softmax and epilogue
@@ -647,8 +619,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_wait_st();
           }
         }
-        // P of two pages ago must have been read before its buffer is rewritten.
-        if (!wait_all(bar(kODone + u), ((gs >> 1) & 1) ^ 1, ctl)) { ok = false; break; }
+        // The page that last used this P buffer must have been read before it is rewritten.
+        if (Lay::kPBufs == 2) {
+          if (!wait_all(bar(kODone + u), ((gs >> 1) & 1) ^ 1, ctl)) { ok = false; break; }
+        } else if (gs > 0 && !wait_all(bar(kODone + (u ^ 1)), ((gs - 1) >> 1) & 1, ctl)) {
+          ok = false;
+          break;
+        }
         if (holds) {
           l *= alpha;
           const float mm = m == -INFINITY ? 0.f : m;  // a row that has seen nothing holds only masked scores
@@ -675,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           l += (s0 + s1) + (s2_ + s3);
 #pragma unroll
           for (int c = 0; c < 4; ++c)
-            *reinterpret_cast<uint4*>(prow + u * Lay::kQBox + (((4 * half + c) ^ (row & 7)) * 16)) =
+            *reinterpret_cast<uint4*>(prow + (u % Lay::kPBufs) * Lay::kQBox + (((4 * half + c) ^ (row & 7)) * 16)) =
                 make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
         }
         fence_proxy_async();
@@ -744,7 +721,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) grid_dep_launch_dependents();  // the combine grid may launch (it waits for this grid's writes)
   tc_fence_before();
   __syncthreads();
-  if (warp == 1) {
+  if (warp == 3) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
@@ -864,23 +841,26 @@ cudaError_t launch_tile(const TileArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   auto encode = tensor_map_encoder();
   if (!encode) return cudaErrorNotSupported;
-  // The cache as [rows, 576] in boxes of 64 rows x 64 dims, q' as [rows of the batch, 576]
-  // in boxes of N rows x 64 dims; every box starts at a multiple of 64 elements.
-  CUtensorMap kv_map, q_map;
-  const cuuint32_t estr[2] = {1, 1};
-  const cuuint64_t strides[1] = {(cuuint64_t)kDQK * 2};
+  // The cache and q' as [9 blocks of 64 dims][rows][64 dims]: one box takes several blocks of
+  // the same rows (a half: 4, the rope: 1, q': 9), each landing as a 128B-swizzled tile.
+  // Every box starts at the beginning of a block.
+  CUtensorMap kv_map, rope_map, q_map;
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const cuuint64_t strides[2] = {(cuuint64_t)kDQK * 2, 128};
   const cuuint64_t kv_rows = (cuuint64_t)(a.block_table ? a.num_pages : a.batch * a.max_blocks) * kPage;
-  const cuuint64_t kv_dims[2] = {(cuuint64_t)kDQK, kv_rows}, q_dims[2] = {(cuuint64_t)kDQK, (cuuint64_t)a.batch * a.rows};
-  const cuuint32_t kv_box[2] = {64, 64}, q_box[2] = {64, N};
-  auto map = [&](CUtensorMap* m, const __nv_bfloat16* p, const cuuint64_t* dims, const cuuint32_t* box) {
-    return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<__nv_bfloat16*>(p), dims, strides, box, estr,
+  auto map = [&](CUtensorMap* m, const __nv_bfloat16* p, cuuint64_t rows, cuuint32_t box_rows, cuuint32_t box_blocks) {
+    const cuuint64_t dims[3] = {64, rows, 9};
+    const cuuint32_t box[3] = {64, box_rows, box_blocks};
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<__nv_bfloat16*>(p), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
   };
-  if (!map(&kv_map, a.kv, kv_dims, kv_box) || !map(&q_map, a.q, q_dims, q_box)) return cudaErrorInvalidValue;
+  if (!map(&kv_map, a.kv, kv_rows, kPage, 4) || !map(&rope_map, a.kv, kv_rows, kPage, 1) ||
+      !map(&q_map, a.q, (cuuint64_t)a.batch * a.rows, N, 9))
+    return cudaErrorInvalidValue;
   const uint64_t limit_ns = (uint64_t)a.wait_limit * 1000000ull;
   e = launch_dependent(decode_tile_kernel<N, kShared>, kShared ? a.num_workers : a.num_workers * a.groups, kThreads,
-                       Layout<N>::kAlloc, stream, kv_map, q_map, a, limit_ns);
+                       Layout<N>::kAlloc, stream, kv_map, rope_map, q_map, a, limit_ns);
   if (e != cudaSuccess) return e;
   const int R = a.batch * a.rows;
   return launch_dependent(combine_tile_kernel<N, kShared>, (R + kCombineWarps - 1) / kCombineWarps, kCombineWarps * 32, 0,
