@@ -87,13 +87,22 @@ def _check(status: int) -> None:
         raise MlaError(status, lib.mla_last_error_message().decode(errors="replace"))
 
 
+# The current stream's handle without a Stream object (0.1 against 3 us, of the 5 us that a
+# small call's launch takes on the host); torch's own generated code takes it the same way.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple | None = None) -> None:
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and (shape is None or t.shape == shape) and t.is_contiguous():
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -204,38 +213,56 @@ def mla_absorb_o(out_latent, w_uv, out, stream=None) -> None:
     mla_decode's fp32, or the bf16 of mla_decode_window and mla_decode_shared (then
     mla_absorb_o_bf16 of the C ABI runs)."""
     B, H = int(out_latent.shape[0]), int(out_latent.shape[1])
-    half = out_latent.dtype == torch.bfloat16
-    _need(out_latent, "out_latent", torch.bfloat16 if half else torch.float32, (B, H, D_LATENT))
+    if out_latent.dtype == torch.bfloat16:
+        dev = torch.cuda.current_device()
+        _check(lib.mla_absorb_o_bf16(_here(out_latent, "out_latent", torch.bfloat16, (B, H, D_LATENT), dev),
+                                     _here(w_uv, "w_uv", torch.bfloat16, (H, D_LATENT, D_V), dev),
+                                     _here(out, "out", torch.float32, (B, H, D_V), dev), B, H, _stream(stream)))
+        return
+    _need(out_latent, "out_latent", torch.float32, (B, H, D_LATENT))
     _need(w_uv, "w_uv", torch.bfloat16, (H, D_LATENT, D_V))
     _need(out, "out", torch.float32, (B, H, D_V))
-    if half:
-        _same_device(out_latent, w_uv, out)
-        _check(lib.mla_absorb_o_bf16(out_latent.data_ptr(), w_uv.data_ptr(), out.data_ptr(), B, H, _stream(stream)))
-        return
     _check(lib.mla_absorb_o(out_latent.data_ptr(), w_uv.data_ptr(), out.data_ptr(), B, H, _stream(stream)))
 
 
-def _same_device(*tensors) -> None:
-    """The library launches on the current device: every tensor must live there."""
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != dev:
-            raise ValueError(f"tensors must be on the current device cuda:{dev}, got {t.device}")
+def _here(t, name, dtype, shape, dev: int) -> int:
+    """_need for a tensor that must also live on the current device ``dev``, where the
+    library launches; returns its address.  One pass of cheap tests, messages on failure."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.is_contiguous()
+            and (shape is None or t.shape == shape)):
+        return t.data_ptr()
+    _need(t, name, dtype, shape)
+    raise ValueError(f"{name} must be on the current device cuda:{dev}, got {t.device}")
 
 
-def _rows_view(t, name, shape):
-    """A bf16 CUDA tensor of ``shape`` whose last dimension is dense; other strides are free."""
+def _rows_view(t, name, shape, dev: int):
+    """Address and strides of a bf16 tensor of ``shape`` on device ``dev`` whose last
+    dimension is dense; other strides are free."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the current device cuda:{dev}, got {t.device}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.stride(-1) != 1 and t.numel():
+    st = t.stride()
+    if st[-1] != 1 and t.numel():
         raise ValueError(f"{name}'s last dimension must be dense")
-    return t.stride()
+    return t.data_ptr(), st
+
+
+def _cache_here(kv_cache, block_table, B: int, dev: int):
+    """_cache_args on the current device: (cache address, max_blocks, num_pages, table address)."""
+    kv = _here(kv_cache, "kv_cache", torch.bfloat16, None, dev)
+    if block_table is None:
+        return (kv, *_cache_args(kv_cache, None, B))
+    bt = _here(block_table, "block_table", torch.int32, None, dev)
+    if kv_cache.dim() != 3 or kv_cache.shape[1] != PAGE or kv_cache.shape[2] != D_QK:
+        raise ValueError("paged kv_cache must be [num_pages, 64, 576]")
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be [B, max_blocks]")
+    return kv, block_table.shape[1], kv_cache.shape[0], bt
 
 
 def mla_append(c_kv, k_rope, kv_cache, block_table, cache_seqlens, cos_sin, cu_tokens=None, q_rope=None, q_out=None,
@@ -248,34 +275,28 @@ def mla_append(c_kv, k_rope, kv_cache, block_table, cache_seqlens, cos_sin, cu_t
     sequence; pos_offset [B] int32 or None."""
     if c_kv.dim() != 2:
         raise ValueError("c_kv must be [N, 512]")
-    N = int(c_kv.shape[0])
-    B = int(cache_seqlens.shape[0])
-    s_c = _rows_view(c_kv, "c_kv", (N, D_LATENT))
-    s_k = _rows_view(k_rope, "k_rope", (N, D_ROPE))
-    _need(cache_seqlens, "cache_seqlens", torch.int32, (B,))
-    _need(cos_sin, "cos_sin", torch.float32)
+    dev = torch.cuda.current_device()
+    N, B = c_kv.shape[0], cache_seqlens.shape[0]
+    p_c, s_c = _rows_view(c_kv, "c_kv", (N, D_LATENT), dev)
+    p_k, s_k = _rows_view(k_rope, "k_rope", (N, D_ROPE), dev)
+    lens = _here(cache_seqlens, "cache_seqlens", torch.int32, (B,), dev)
+    table = _here(cos_sin, "cos_sin", torch.float32, None, dev)
     if cos_sin.dim() != 2 or cos_sin.shape[1] != D_ROPE:
         raise ValueError("cos_sin must be [max_pos, 64]")
-    if cu_tokens is not None:
-        _need(cu_tokens, "cu_tokens", torch.int32, (B + 1,))
-    if pos_offset is not None:
-        _need(pos_offset, "pos_offset", torch.int32, (B,))
+    cu = None if cu_tokens is None else _here(cu_tokens, "cu_tokens", torch.int32, (B + 1,), dev)
+    off = None if pos_offset is None else _here(pos_offset, "pos_offset", torch.int32, (B,), dev)
     if (q_rope is None) != (q_out is None):
         raise ValueError("q_rope and q_out go together")
-    H, s_q, s_o = 0, (0, 0), (0, 0)
+    H, p_q, p_o, s_q, s_o = 0, None, None, (0, 0), (0, 0)
     if q_rope is not None:
         if q_rope.dim() != 3:
             raise ValueError("q_rope must be [N, H, 64]")
-        H = int(q_rope.shape[1])
-        s_q = _rows_view(q_rope, "q_rope", (N, H, D_ROPE))
-        s_o = _rows_view(q_out, "q_out", (N, H, D_ROPE))
-    max_blocks, num_pages, bt = _cache_args(kv_cache, block_table, B)
-    _same_device(c_kv, k_rope, kv_cache, block_table, cache_seqlens, cos_sin, cu_tokens, q_rope, q_out, pos_offset)
-    ptr = lambda t: None if t is None else t.data_ptr()
-    _check(lib.mla_append(c_kv.data_ptr(), k_rope.data_ptr(), ptr(q_rope), ptr(q_out), cos_sin.data_ptr(), ptr(cu_tokens),
-                          cache_seqlens.data_ptr(), ptr(pos_offset), bt, kv_cache.data_ptr(), s_c[0], s_k[0], s_q[0],
-                          s_q[1], s_o[0], s_o[1], N, B, H, num_pages, max_blocks, int(cos_sin.shape[0]),
-                          1 if interleaved else 0, _stream(stream)))
+        H = q_rope.shape[1]
+        p_q, s_q = _rows_view(q_rope, "q_rope", (N, H, D_ROPE), dev)
+        p_o, s_o = _rows_view(q_out, "q_out", (N, H, D_ROPE), dev)
+    kv, max_blocks, num_pages, bt = _cache_here(kv_cache, block_table, B, dev)
+    _check(lib.mla_append(p_c, p_k, p_q, p_o, table, cu, lens, off, bt, kv, s_c[0], s_k[0], s_q[0], s_q[1], s_o[0], s_o[1], N,
+                          B, H, num_pages, max_blocks, cos_sin.shape[0], 1 if interleaved else 0, _stream(stream)))
 
 
 def _query_shape(q):
@@ -283,15 +304,16 @@ def _query_shape(q):
     if q.dim() == 3:
         return (q.shape[0], 1, q.shape[1]), (q.shape[0], q.shape[1])
     if q.dim() == 4:
-        return tuple(q.shape[:3]), tuple(q.shape[:3])
+        rows = tuple(q.shape[:3])
+        return rows, rows
     raise ValueError("q must be [B, H, 576] or [B, s_q, H, 576]")
 
 
-def _workspace(workspace, size, stream, device):
+def _workspace(workspace, size, stream, device, dev):
     """A caller's workspace, or one from torch's allocator that the call alone uses: taken
     on the launching stream, so its reuse is ordered after this call."""
     if workspace is not None:
-        _need(workspace, "workspace", torch.uint8)
+        _here(workspace, "workspace", torch.uint8, None, dev)
         return workspace
     if stream is None:
         return torch.empty(size, dtype=torch.uint8, device=device)
@@ -308,15 +330,14 @@ def mla_decode_window(q, kv_cache, block_table, cache_seqlens, out, lse, softmax
     mla_decode_window_workspace_size(B, s_q, H) bytes, or None to take one from torch's
     allocator for this call."""
     (B, SQ, H), rows = _query_shape(q)
-    _need(q, "q", torch.bfloat16, rows + (D_QK,))
-    _need(cache_seqlens, "cache_seqlens", torch.int32, (B,))
-    _need(out, "out", torch.bfloat16, rows + (D_LATENT,))
-    _need(lse, "lse", torch.float32, rows)
-    max_blocks, num_pages, bt = _cache_args(kv_cache, block_table, B)
-    _same_device(q, kv_cache, block_table, cache_seqlens, out, lse, workspace)
-    ws = _workspace(workspace, lib.mla_decode_window_workspace_size(B, SQ, H), stream, q.device)
-    _check(lib.mla_decode_window(q.data_ptr(), kv_cache.data_ptr(), bt, cache_seqlens.data_ptr(), out.data_ptr(),
-                                 lse.data_ptr(), B, SQ, H, num_pages, max_blocks, window, sinks, softmax_scale,
+    dev = torch.cuda.current_device()
+    p_q = _here(q, "q", torch.bfloat16, rows + (D_QK,), dev)
+    lens = _here(cache_seqlens, "cache_seqlens", torch.int32, (B,), dev)
+    p_o = _here(out, "out", torch.bfloat16, rows + (D_LATENT,), dev)
+    p_l = _here(lse, "lse", torch.float32, rows, dev)
+    kv, max_blocks, num_pages, bt = _cache_here(kv_cache, block_table, B, dev)
+    ws = _workspace(workspace, lib.mla_decode_window_workspace_size(B, SQ, H), stream, q.device, dev)
+    _check(lib.mla_decode_window(p_q, kv, bt, lens, p_o, p_l, B, SQ, H, num_pages, max_blocks, window, sinks, softmax_scale,
                                  ws.data_ptr(), ws.numel(), _stream(stream)))
 
 
@@ -331,23 +352,21 @@ def mla_decode_shared(q, kv_cache, prefix_table, prefix_len, block_table, cache_
     [B,max_blocks] and cache_seqlens [B] int32 each sequence's own tokens; q, out, lse,
     workspace as in mla_decode_window (mla_decode_shared_workspace_size)."""
     (B, SQ, H), rows = _query_shape(q)
-    _need(q, "q", torch.bfloat16, rows + (D_QK,))
-    _need(prefix_table, "prefix_table", torch.int32)
+    dev = torch.cuda.current_device()
+    p_q = _here(q, "q", torch.bfloat16, rows + (D_QK,), dev)
+    ptab = _here(prefix_table, "prefix_table", torch.int32, None, dev)
     if prefix_table.dim() != 1:
         raise ValueError("prefix_table must be [prefix_blocks]")
-    _need(prefix_len, "prefix_len", torch.int32, (1,))
-    _need(cache_seqlens, "cache_seqlens", torch.int32, (B,))
-    _need(out, "out", torch.bfloat16, rows + (D_LATENT,))
-    _need(lse, "lse", torch.float32, rows)
+    plen = _here(prefix_len, "prefix_len", torch.int32, (1,), dev)
+    lens = _here(cache_seqlens, "cache_seqlens", torch.int32, (B,), dev)
+    p_o = _here(out, "out", torch.bfloat16, rows + (D_LATENT,), dev)
+    p_l = _here(lse, "lse", torch.float32, rows, dev)
     if block_table is None:
         raise ValueError("block_table is needed: the shared prefix and the own tokens are pages of one cache")
-    max_blocks, num_pages, bt = _cache_args(kv_cache, block_table, B)
-    _same_device(q, kv_cache, prefix_table, prefix_len, block_table, cache_seqlens, out, lse, workspace)
-    ws = _workspace(workspace, lib.mla_decode_shared_workspace_size(B, SQ, H), stream, q.device)
-    _check(lib.mla_decode_shared(q.data_ptr(), kv_cache.data_ptr(), prefix_table.data_ptr(), prefix_len.data_ptr(), bt,
-                                 cache_seqlens.data_ptr(), out.data_ptr(), lse.data_ptr(), B, SQ, H, num_pages,
-                                 prefix_table.shape[0], max_blocks, softmax_scale, ws.data_ptr(), ws.numel(),
-                                 _stream(stream)))
+    kv, max_blocks, num_pages, bt = _cache_here(kv_cache, block_table, B, dev)
+    ws = _workspace(workspace, lib.mla_decode_shared_workspace_size(B, SQ, H), stream, q.device, dev)
+    _check(lib.mla_decode_shared(p_q, kv, ptab, plen, bt, lens, p_o, p_l, B, SQ, H, num_pages, prefix_table.shape[0],
+                                 max_blocks, softmax_scale, ws.data_ptr(), ws.numel(), _stream(stream)))
 
 
 def mla_decode_shared_workspace_size(batch: int, s_q: int, heads: int) -> int:
