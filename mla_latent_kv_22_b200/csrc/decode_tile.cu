@@ -41,7 +41,7 @@
 #include "mla_device.cuh"
 #include "mla_internal.h"
 #include "sm100_ptx.cuh"
-#include "worker_range.cuh"
+#include "tile_tasks.cuh"
 
 namespace mla {
 namespace {
@@ -139,114 +139,67 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, uint64
   }
 }
 
-// ---------------------------------------------------------------- tasks
-// The pages of a task: page p of its list is page real(p) of its table; the first `ns`
-// hold the sinks, the rest run from the window's first page to the last.
-struct Span {
-  int T, n, ns, skip;
-  int hole0, hole1;  // tokens [hole0, hole1) are in no query's sight (between sinks and window)
-  __device__ __forceinline__ int real(int p) const { return p < ns ? p : p + skip; }
-};
-
-__device__ __forceinline__ Span window_span(const TileArgs& a, int T) {
-  Span s{T, 0, 0, 0, 0, 0};
-  if (T <= 0 || T > a.max_blocks * kPage) return s;
-  const int first = max(0, T - a.s_q - a.window + 1);
-  const int sinks = min(a.sinks, T);
-  s.ns = (sinks + kPage - 1) / kPage;
-  s.skip = max(0, first / kPage - s.ns);
-  s.n = (T + kPage - 1) / kPage - s.skip;
-  s.hole0 = sinks;
-  s.hole1 = first;
-  return s;
+// Lane 4g + i gives v[j] of row j and takes v[j] = row i of lane 4g + j.
+__device__ __forceinline__ void transpose4(float (&v)[4], int lane) {
+  const bool b0 = lane & 1, b1 = lane & 2;
+#pragma unroll
+  for (int p = 0; p < 4; p += 2) {
+    const float got = __shfl_xor_sync(0xffffffffu, b0 ? v[p] : v[p + 1], 1);
+    if (b0) v[p] = got;
+    else v[p + 1] = got;
+  }
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    const float got = __shfl_xor_sync(0xffffffffu, b1 ? v[p] : v[p + 2], 2);
+    if (b1) v[p] = got;
+    else v[p + 2] = got;
+  }
 }
 
-template <bool kShared>
-struct TaskLengths {
-  const TileArgs* a;
-  __device__ __forceinline__ int raw(int t) const {
-    if (!kShared) return a->seqlens[t];
-    return t < a->tiles ? *a->prefix_len : a->seqlens[(t - a->tiles) / a->groups];
-  }
-  __device__ __forceinline__ int cap(int t) const { return kShared && t < a->tiles ? a->prefix_blocks : a->max_blocks; }
-  __device__ __forceinline__ bool bad(int t) const {
-    const int T = raw(t);
-    return T < 0 || T > cap(t) * kPage;
-  }
-  __device__ __forceinline__ int pages(int t) const {
-    const int T = raw(t);
-    if (!kShared) return window_span(*a, T).n;
-    return (T < 0 || T > cap(t) * kPage) ? 0 : (T + kPage - 1) / kPage;
-  }
-};
-
-struct Task {
-  Span s;
-  const int32_t* table;  // null: page = base + real
-  int base;
-  int row0, live;  // first query row of the whole batch's, rows of the tile
-  int srow;        // row0 within its sequence (window, own tokens)
-};
-
-template <int N, bool kShared>
-__device__ __forceinline__ Task load_task(const TileArgs& a, int t, int g) {
-  Task k;
-  k.base = 0;
-  if (kShared && t < a.tiles) {
-    const int T = *a.prefix_len;
-    k.s = Span{T, (T + kPage - 1) / kPage, (T + kPage - 1) / kPage, 0, 0, 0};
-    k.table = a.prefix_table;
-    k.row0 = t * N;
-    k.live = min(N, a.batch * a.rows - k.row0);
-    k.srow = 0;
-    return k;
-  }
-  const int b = kShared ? (t - a.tiles) / a.groups : t;
-  if (kShared) g = (t - a.tiles) % a.groups;
-  const int T = a.seqlens[b];
-  k.s = kShared ? Span{T, (T + kPage - 1) / kPage, (T + kPage - 1) / kPage, 0, 0, 0} : window_span(a, T);
-  k.table = a.block_table ? a.block_table + (size_t)b * a.max_blocks : nullptr;
-  k.base = b * a.max_blocks;
-  k.srow = g * N;
-  k.row0 = b * a.rows + k.srow;
-  k.live = min(N, a.rows - k.srow);
-  return k;
-}
-
-struct Piece {
-  int t, pa, pe;
-};
-
-// Iterates the pieces of a worker's range in schedule order.
-template <bool kShared>
-struct PieceIter {
-  WorkerRange rg;
-  int t;
-  __device__ explicit PieceIter(const volatile WorkerRange& r) : rg{r.b0, r.p0, r.b1, r.p1}, t(r.b0) {}
-  __device__ bool next(Piece& pc, const TileArgs& a) {
-    if (rg.b0 < 0) return false;
-    const TaskLengths<kShared> len{&a};
-    while (t <= rg.b1) {
-      const int cur = t++;
-      const int pa = cur == rg.b0 ? rg.p0 : 0;
-      const int pe = cur == rg.b1 ? rg.p1 : len.pages(cur);
-      if (pa < pe) {
-        pc = {cur, pa, pe};
-        return true;
-      }
+// One 16-column block of O^T leaves for out (bf16) or a partial (fp32): TMEM column e of
+// `taddr` is row e, lanes are dims.  inv[e] is the row's factor, `live` the number of rows
+// stored, ob / po the address of (row lane % 4, the lane quad's first dim).  Four lanes
+// trade four rows of their dims for one row's four dims each, so that a store covers 128
+// (fp32) or 64 (bf16) contiguous bytes of four rows.
+template <bool kDirect>
+__device__ __forceinline__ void store_o16(const uint32_t (&r)[16], const float* inv, int live, __nv_bfloat16* ob, float* po,
+                                          int lane) {
+  const int i = lane & 3;
+#pragma unroll
+  for (int e = 0; e < 16; e += 4) {
+    float v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = __uint_as_float(r[e + j]);
+    transpose4(v, lane);
+    const float f = inv[e + i];
+    if (e + i < live) {
+      if (kDirect)
+        *reinterpret_cast<uint2*>(ob + e * kDLatent) = make_uint2(pack_bf16x2(v[0] * f, v[1] * f), pack_bf16x2(v[2] * f, v[3] * f));
+      else
+        *reinterpret_cast<float4*>(po + e * kDLatent) = make_float4(v[0] * f, v[1] * f, v[2] * f, v[3] * f);
     }
-    return false;
   }
-};
-
-// Whether some row of table page `real` is in no query's sight.
-__device__ __forceinline__ bool page_dirty(const Span& s, int real) {
-  const int t0 = real * kPage;
-  return s.T < t0 + kPage || (max(s.hole0, t0) < min(s.hole1, t0 + kPage));
 }
 
-// Bits [0, x) of a word.
-__device__ __forceinline__ uint32_t below(int x) { return x <= 0 ? 0u : x >= 32 ? 0xffffffffu : (1u << x) - 1u; }
+// All of a warp's O^T: four accumulators of N columns from `taddr` on, 128 dims apart, of
+// which the warp holds 32 from dim0 on; rows below `live` are stored.  The next block's
+// TMEM load flies under the current one's stores.
+template <int N, bool kDirect>
+__device__ __forceinline__ void store_o(uint32_t taddr, const float* inv, int live, __nv_bfloat16* out, float* part, int dim0,
+                                        int lane) {
+  constexpr int kN = 4 * (N / 16);
+  const size_t at = (size_t)(lane & 3) * kDLatent + dim0 + (lane & ~3);
+  uint32_t r[2][16];
+  tmem_ld16(taddr, r[0]);
+#pragma unroll 2
+  for (int n = 0; n < kN; ++n) {
+    tmem_wait_ld();
+    const int m = n / (N / 16), r0 = 16 * (n % (N / 16));
+    if (n + 1 < kN) tmem_ld16(taddr + 16 * (n + 1), r[(n + 1) & 1]);
+    const size_t off = at + (size_t)r0 * kDLatent + 128 * m;
+    store_o16<kDirect>(r[n & 1], inv + r0, live - r0, out + off, part + off, lane);
+  }
+}
 
 template <int N, bool kShared>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -308,8 +261,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Everything above overlaps the previous grid on the stream; from here on its writes
   // (the lengths, q', the tables, the cache) are visible.
   grid_dep_wait();
-  derive_range(TaskLengths<kShared>{&a}, kShared ? a.tiles + a.batch * a.groups : a.batch, a.num_workers, a.min_pages, 1,
-               a.whole_slack, a.piece_cost, a.task, a.err, w, range_s);
+  derive_range(TaskLengths<kShared>{&a}, kShared ? a.tiles + a.batch * a.groups : a.batch, a.num_workers, a.min_pages,
+               a.granule, a.whole_slack, a.piece_cost, a.task, a.err, w, range_s);
   const uint32_t tmem = tmem_base_s;
   const Ctl ctl{a.err, &abort_s, limit_ns};
 
@@ -343,13 +296,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool dirty = page_dirty(k.s, k.s.real(p));
 #pragma unroll 1
         for (int m = 0; m < 2; ++m) {
-          // The page's rope rides on its second half; its slot is free once the scores of
-          // two pages ago are done.
-          if (!wait_all(bar(kEmpty + slot), phase, ctl) ||
-              (m == 1 && !wait_all(bar(kSFull + (g & 1)), ((g >> 1) & 1) ^ 1, ctl))) {
-            ok = false;
-            break;
-          }
+          // The page's rope rides on its second half, whose ring slot was last held by the
+          // page two before (4 or 5 slots): with that page's second product done, its
+          // scores are, and its rope slot is free.
+          if (!wait_all(bar(kEmpty + slot), phase, ctl)) { ok = false; break; }
           const uint32_t bit = 1u << slot;
           if (a.withhold_arrive && blockIdx.x == 0 && fills == 1) {
             withheld = slot;  // timeout test: this fill never completes
@@ -686,29 +636,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!wait_all(bar(kODone + (ge & 1)), (ge >> 1) & 1, ctl)) { ok = false; break; }
       tc_fence_after();
-#pragma unroll 1
-      for (int cc = 0; cc < 4 * N; cc += 16) {
-        const int r0 = cc & (N - 1), dim = 128 * (cc / N) + 32 * q + lane;
-        uint32_t r[16];
-        tmem_ld16(tmem + lane_addr + kColO + cc, r);
-        tmem_wait_ld();
-        if (direct) {
-          // Two lanes trade halves of two rows, so that each stores two dims of one.
-#pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            const float v0 = __uint_as_float(r[e]) * al_s[0][r0 + e], v1 = __uint_as_float(r[e + 1]) * al_s[0][r0 + e + 1];
-            const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? v0 : v1, 1);
-            const int orow = r0 + e + (lane & 1);
-            if (orow < k.live)
-              *reinterpret_cast<uint32_t*>(a.out + (prow0 + orow) * kDLatent + (dim & ~1)) =
-                  lane & 1 ? pack_bf16x2(got, v1) : pack_bf16x2(v0, got);
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (r0 + e < k.live) a.part_o[(prow0 + r0 + e) * kDLatent + dim] = __uint_as_float(r[e]) * al_s[0][r0 + e];
-        }
-      }
+      if (direct)
+        store_o<N, true>(tmem + lane_addr + kColO, al_s[0], k.live, a.out + prow0 * kDLatent, nullptr, 32 * q, lane);
+      else
+        store_o<N, false>(tmem + lane_addr + kColO, al_s[0], k.live, nullptr, a.part_o + prow0 * kDLatent, 32 * q, lane);
       tc_fence_before();
       if (!meet()) { ok = false; break; }  // al_s may be rewritten
       if (lane == 0) mbar_arrive(bar(kOFree));
@@ -732,12 +663,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 // the prefix and against the sequence's own tokens, by their lse, in that fixed order.
 constexpr int kCombineWarps = 4;
 
-template <int N, bool kShared>
+template <bool kShared>
 __global__ void __launch_bounds__(kCombineWarps * 32) combine_tile_kernel(const __grid_constant__ TileArgs a) {
   grid_dep_launch_dependents();
   grid_dep_wait();
   const int lane = threadIdx.x & 31;
-  const int R = a.batch * a.rows;
+  const int R = a.batch * a.rows, N = a.row_tile;
   const int gr = blockIdx.x * kCombineWarps + (threadIdx.x >> 5);
   if (gr >= R) return;
   const int b = gr / a.rows, r = gr - b * a.rows, g = r / N, rr = r % N;
@@ -817,54 +748,16 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_tile_kernel(const 
   if (lane == 0) a.lse[gr] = L + logf(wsum);
 }
 
-// A launch as a programmatic dependent of the grid before it on the stream.
-template <typename... Params, typename... Args>
-cudaError_t launch_dependent(void (*kernel)(Params...), int grid, int threads, int smem, cudaStream_t stream,
-                             const Args&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, 1, 1);
-  cfg.blockDim = dim3(threads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 template <int N, bool kShared>
 cudaError_t launch_tile(const TileArgs& a, cudaStream_t stream) {
   static bool done[64] = {};
   cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void*>(decode_tile_kernel<N, kShared>), Layout<N>::kAlloc, done);
   if (e != cudaSuccess) return e;
-  auto encode = tensor_map_encoder();
-  if (!encode) return cudaErrorNotSupported;
-  // The cache and q' as [9 blocks of 64 dims][rows][64 dims]: one box takes several blocks of
-  // the same rows (a half: 4, the rope: 1, q': 9), each landing as a 128B-swizzled tile.
-  // Every box starts at the beginning of a block.
   CUtensorMap kv_map, rope_map, q_map;
-  const cuuint32_t estr[3] = {1, 1, 1};
-  const cuuint64_t strides[2] = {(cuuint64_t)kDQK * 2, 128};
-  const cuuint64_t kv_rows = (cuuint64_t)(a.block_table ? a.num_pages : a.batch * a.max_blocks) * kPage;
-  auto map = [&](CUtensorMap* m, const __nv_bfloat16* p, cuuint64_t rows, cuuint32_t box_rows, cuuint32_t box_blocks) {
-    const cuuint64_t dims[3] = {64, rows, 9};
-    const cuuint32_t box[3] = {64, box_rows, box_blocks};
-    return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<__nv_bfloat16*>(p), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-  };
-  if (!map(&kv_map, a.kv, kv_rows, kPage, 4) || !map(&rope_map, a.kv, kv_rows, kPage, 1) ||
-      !map(&q_map, a.q, (cuuint64_t)a.batch * a.rows, N, 9))
-    return cudaErrorInvalidValue;
+  if (!tile_maps(a, N, 9, &kv_map, &rope_map, &q_map)) return cudaErrorInvalidValue;
   const uint64_t limit_ns = (uint64_t)a.wait_limit * 1000000ull;
-  e = launch_dependent(decode_tile_kernel<N, kShared>, kShared ? a.num_workers : a.num_workers * a.groups, kThreads,
-                       Layout<N>::kAlloc, stream, kv_map, rope_map, q_map, a, limit_ns);
-  if (e != cudaSuccess) return e;
-  const int R = a.batch * a.rows;
-  return launch_dependent(combine_tile_kernel<N, kShared>, (R + kCombineWarps - 1) / kCombineWarps, kCombineWarps * 32, 0,
-                          stream, a);
+  return launch_dependent(decode_tile_kernel<N, kShared>, kShared ? a.num_workers : a.num_workers * a.groups, kThreads,
+                          Layout<N>::kAlloc, stream, kv_map, rope_map, q_map, a, limit_ns);
 }
 
 }  // namespace
@@ -872,15 +765,15 @@ cudaError_t launch_tile(const TileArgs& a, cudaStream_t stream) {
 size_t plan_tile(TileArgs* a, int sm_count, int forced_workers, void* base) {
   const bool shared = a->prefix_len != nullptr;
   const long long R = (long long)a->batch * a->rows;
-  // The fewest tiles of at most 64 rows, then the narrowest tile that gives as few: narrow
-  // tiles leave more shared memory to the load ring.  A prefix is read by tiles of the
-  // whole batch's rows, so there the batch's rows count.
+  // Up to 64 rows, the narrowest tile that holds them on one CTA: narrow tiles leave more
+  // shared memory to the load ring.  More rows take tiles of 128 on a CTA pair.  A prefix
+  // is read by tiles of the whole batch's rows, so there the batch's rows count.
   const long long all = shared ? R : a->rows;
-  const int tiles = (int)((all + 63) / 64), per = (int)((all + tiles - 1) / tiles);
-  a->row_tile = per <= 16 ? 16 : per <= 32 ? 32 : 64;
+  a->row_tile = all <= 16 ? 16 : all <= 32 ? 32 : all <= 64 ? 64 : 128;
   a->groups = (a->rows + a->row_tile - 1) / a->row_tile;
   a->tiles = shared ? (int)((R + a->row_tile - 1) / a->row_tile) : 0;
-  a->num_workers = shared ? sm_count : std::max(1, sm_count / a->groups);
+  const int workers = a->row_tile == 128 ? sm_count / 2 : sm_count;
+  a->num_workers = std::max(1, shared ? workers : workers / a->groups);
   if (forced_workers > 0) a->num_workers = forced_workers;
   const size_t tasks = shared ? (size_t)a->tiles + (size_t)a->batch * a->groups : (size_t)a->batch;
   const size_t rows = shared ? (size_t)2 * a->num_workers * a->row_tile + 2 * (size_t)R
@@ -900,19 +793,36 @@ size_t plan_tile(TileArgs* a, int sm_count, int forced_workers, void* base) {
 void tile_schedule(TileArgs* a) {
   const int mp = knob_value(MLA_KNOB_MIN_PAGES), pc = knob_value(MLA_KNOB_PIECE_COST);
   const int policy = knob_value(MLA_KNOB_SPLIT_POLICY);
+  a->granule = a->row_tile == 128 ? 2 : 1;  // pages per step
   a->min_pages = mp > 0 ? mp : 2;
-  a->piece_cost = pc > 0 ? std::min(pc - 1, kMaxPieceCost) : 3;
-  a->whole_slack = knob_value(MLA_KNOB_NUM_WORKERS) > 0 || policy == 1 ? -1 : policy == 2 ? 1 << 30 : 2;
+  // A piece costs a pair as much as 10 of its pages, a single CTA as much as 3 (us at 4 / 7 /
+  // 10 / 13 pages: pair, 64 sequences of 128 heads sharing 8,192 tokens 161 / 137 / 146 / 154,
+  // 32 sharing 2,000 44 / 37 / 36 / 38; single, at 0 / 3 / 6 / 9, 16 heads of 128 sequences
+  // sharing 1,000 47 / 41 / 41 / 43, 32 heads over a window of 4,096 44 / 42 / 40 / 39).
+  a->piece_cost = pc > 0 ? std::min(pc - 1, kMaxPieceCost) : a->row_tile == 128 ? 10 : 3;
+  // Sequences run whole when splitting them would save less than its piece costs: up to 12
+  // pages for a pair (128 heads, whole / split us: 64 windows of 65 pages 75 / 86, of 1 to 34
+  // pages 47 / 53; 16 windows of 66 pages for two queries of 64 heads 59 / 37).
+  const int slack = a->row_tile == 128 ? 12 : 2;
+  a->whole_slack = knob_value(MLA_KNOB_NUM_WORKERS) > 0 || policy == 1 ? -1 : policy == 2 ? 1 << 30 : slack;
 }
 
 cudaError_t launch_decode_tile(const TileArgs& a, cudaStream_t stream) {
-  if (a.prefix_len)
-    return a.row_tile == 16   ? launch_tile<16, true>(a, stream)
-           : a.row_tile == 32 ? launch_tile<32, true>(a, stream)
-                              : launch_tile<64, true>(a, stream);
-  return a.row_tile == 16   ? launch_tile<16, false>(a, stream)
-         : a.row_tile == 32 ? launch_tile<32, false>(a, stream)
-                            : launch_tile<64, false>(a, stream);
+  const bool shared = a.prefix_len != nullptr;
+  cudaError_t e;
+  if (a.row_tile == 128) e = launch_decode_tile_pair(a, stream);
+  else if (shared)
+    e = a.row_tile == 16   ? launch_tile<16, true>(a, stream)
+        : a.row_tile == 32 ? launch_tile<32, true>(a, stream)
+                           : launch_tile<64, true>(a, stream);
+  else
+    e = a.row_tile == 16   ? launch_tile<16, false>(a, stream)
+        : a.row_tile == 32 ? launch_tile<32, false>(a, stream)
+                           : launch_tile<64, false>(a, stream);
+  if (e != cudaSuccess) return e;
+  const int grid = (a.batch * a.rows + kCombineWarps - 1) / kCombineWarps;
+  return shared ? launch_dependent(combine_tile_kernel<true>, grid, kCombineWarps * 32, 0, stream, a)
+                : launch_dependent(combine_tile_kernel<false>, grid, kCombineWarps * 32, 0, stream, a);
 }
 
 }  // namespace mla

@@ -104,10 +104,10 @@ int decode_pair_max_workers(int sm_count);
 cudaError_t launch_decode(int kernel, const DecodeArgs& a, cudaStream_t stream);
 int decode_granule(int kernel);
 
-// Sliding-window and shared-prefix decode (decode_tile.cu): one CTA per worker, query
-// rows in tiles of row_tile (16, 32 or 64).  The schedule's entries ("tasks") are, for a
+// Sliding-window and shared-prefix decode: query rows in tiles of row_tile (16, 32 or 64
+// with one CTA per worker, decode_tile.cu, or 128 with a CTA pair, decode_tile_pair.cu).  The schedule's entries ("tasks") are, for a
 // window, the sequences (worker w of group g walks the pages for rows [g row_tile, +) of
-// each sequence, so the `groups` CTAs of one worker read the same pages side by side);
+// each sequence, so the `groups` CTAs or pairs of one worker read the same pages side by side);
 // for a shared prefix, first the prefix once for each of the `tiles` row tiles of the
 // whole batch, then each sequence's own tokens once for each of its groups.
 struct TileArgs {
@@ -132,7 +132,7 @@ struct TileArgs {
   float* part_lse;
   float* part_o;
   int num_workers;
-  int min_pages, whole_slack, piece_cost;
+  int min_pages, granule, whole_slack, piece_cost;
   int wait_limit, withhold_arrive;
 };
 
@@ -143,6 +143,7 @@ size_t plan_tile(TileArgs* a, int sm_count, int forced_workers, void* base);
 // Sets the schedule's constants for the current knobs.
 void tile_schedule(TileArgs* a);
 cudaError_t launch_decode_tile(const TileArgs& a, cudaStream_t stream);
+cudaError_t launch_decode_tile_pair(const TileArgs& a, cudaStream_t stream);  // the decode grid of 128-row tiles
 
 // Cache append with position rotation (append.cu).
 struct AppendArgs {

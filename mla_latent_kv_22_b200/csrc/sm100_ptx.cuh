@@ -26,6 +26,13 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
+// The same with CTA-scope release, for an arrival that only publishes what the tensor cores
+// read: tensor memory (ordered by tcgen05.fence::before_thread_sync) and shared memory
+// already handed to the async proxy (fence.proxy.async).  A cluster-scope release waits for
+// every outstanding access of the thread, ~700 ns measured in decode_tile_pair.cu.
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
 __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
@@ -328,7 +335,31 @@ __device__ __forceinline__ void mma_pair_x4_elect(uint32_t d_tmem, uint64_t a_de
       "n"(kBStep), "n"(2 * kBStep), "n"(3 * kBStep)
       : "memory");
 }
-// The same with A in tensor memory (pair-wide layout: each CTA holds its rows of A in
+// Two accumulators `kDStep` columns apart over the same four steps of A, B `kBOther` 16-byte
+// units apart: the second MMA of a step takes A from the collector instead of shared memory.
+template <uint32_t kAStep, uint32_t kBStep, uint32_t kDStep, uint32_t kBOther>
+__device__ __forceinline__ void mma_pair_x4x2_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                                    uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred acc, one, e;\n .reg .b32 d2;\n .reg .b64 a1, a2, a3, b1, b2, b3, c0, c1, c2, c3;\n"
+      " setp.ne.b32 acc, %4, 0;\n setp.eq.u32 one, 1, 1;\n elect.sync _|e, 0xffffffff;\n"
+      " add.u32 d2, %0, %11;\n"
+      " add.u64 a1, %1, %5;\n add.u64 a2, %1, %6;\n add.u64 a3, %1, %7;\n"
+      " add.u64 b1, %2, %8;\n add.u64 b2, %2, %9;\n add.u64 b3, %2, %10;\n"
+      " add.u64 c0, %2, %12;\n add.u64 c1, b1, %12;\n add.u64 c2, b2, %12;\n add.u64 c3, b3, %12;\n"
+      " @e tcgen05.mma.cta_group::2.kind::f16.collector::a::fill [%0], %1, %2, %3, acc;\n"
+      " @e tcgen05.mma.cta_group::2.kind::f16.collector::a::lastuse [d2], %1, c0, %3, acc;\n"
+      " @e tcgen05.mma.cta_group::2.kind::f16.collector::a::fill [%0], a1, b1, %3, one;\n"
+      " @e tcgen05.mma.cta_group::2.kind::f16.collector::a::lastuse [d2], a1, c1, %3, one;\n"
+      " @e tcgen05.mma.cta_group::2.kind::f16.collector::a::fill [%0], a2, b2, %3, one;\n"
+      " @e tcgen05.mma.cta_group::2.kind::f16.collector::a::lastuse [d2], a2, c2, %3, one;\n"
+      " @e tcgen05.mma.cta_group::2.kind::f16.collector::a::fill [%0], a3, b3, %3, one;\n"
+      " @e tcgen05.mma.cta_group::2.kind::f16.collector::a::lastuse [d2], a3, c3, %3, one;\n}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "n"(kAStep), "n"(2 * kAStep), "n"(3 * kAStep), "n"(kBStep),
+      "n"(2 * kBStep), "n"(3 * kBStep), "n"(kDStep), "n"(kBOther)
+      : "memory");
+}
+// Four pair-wide MMAs along K with A in tensor memory (pair-wide layout: each CTA holds its rows of A in
 // lanes 0-63 and again in lanes 64-127), stepped by 8 columns (16 bf16) along K.
 template <uint32_t kBStep>
 __device__ __forceinline__ void mma_pair_ts_x4_elect(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
@@ -369,6 +400,14 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* map, 
       "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
       "[%4];" ::"r"(dst),
       "l"(map), "r"(x), "r"(y), "r"(bar_cluster)
+      : "memory");
+}
+// 3-D form of the same.
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void* map, int x, int y, int z, uint32_t bar_cluster) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar_cluster)
       : "memory");
 }
 // Named barrier over `nthreads` threads (a multiple of 32) of this CTA.
