@@ -14,16 +14,17 @@
 // tensor-parallel shard) run at the speed of the loads, and the rows of many sequences are
 // packed into tiles of 64 where they share the tokens (a common prefix).
 //
-// Roles (256 threads).  Warp 0: page loads (TMA), two 32 KB halves of 256 latent dims per
-// page into a ring, freed by the second product, and the rope dims into two 8 KB slots,
-// freed by the first.  Warp 1: q' loads and the first product's MMAs.  Warp 2: zeroes the
-// rows of a page that no query of the sequence sees (past its end, or between the sinks
-// and the window), where a masked P of 0 would meet whatever the cache holds.  Warp 3:
-// tensor memory and the second product's MMAs.  (One warp issuing both products was bound
-// by its own instruction stream: 52 MMAs of ~35 cycles and 14 waits and commits of
-// 70-110 a page; two warps, and one commit per half, overlap them.)  Warps 4-7: softmax
-// of the 16 rows in their TMEM quadrant (two threads per row, 32 tokens each) and the
-// epilogue.
+// Roles (384 threads).  Warps 0-3: softmax of the 16 rows in their TMEM quadrant (two threads
+// per row, 32 tokens each).  Warps 4-7: store a piece's O, with up to 32 rows from a second
+// accumulator while the next piece runs.  Warp 8: page loads (TMA), two 32 KB halves of 256
+// latent dims per page into a ring, freed by the second product, and the rope dims into two
+// 8 KB slots, freed by the first.  Warp 9: q' loads and the first product's MMAs.  Warp 10:
+// zeroes the rows of a page that no query of the sequence sees (past its end, or between the
+// sinks and the window), where a masked P of 0 would meet whatever the cache holds.  Warp 11:
+// tensor memory and the second product's MMAs.  (One warp issuing both products was bound by
+// its own instruction stream: 52 MMAs of ~35 cycles and 14 waits and commits of 70-110 a
+// page; two warps, and one commit per half, overlap them.)  The first warps also write the
+// schedule's records, which the loads should not wait for.
 //
 // The running maximum is lazy as in decode_pair.cu: O and the sum are rescaled only when a
 // page's maximum exceeds the reference by more than 2^8.  Since O's lanes are dims, all
@@ -48,12 +49,13 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 384;
+constexpr int kLoad = 8, kScores = 9, kClean = 10, kValues = 11;  // warps; 0-3 softmax, 4-7 store
 constexpr int kBox = 8192;            // [64 tokens x 64 bf16], 128B swizzle
 constexpr int kSlotBytes = 4 * kBox;  // a ring slot: one half (256 latent dims) of a page
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColO = 0, kColS = 256;  // O^T: block m at 4 columns-of-N m; S: two buffers of 64 columns
+constexpr uint32_t kColO = 0, kColS = 256;  // O^T: block m at column N m of its buffer; S: two buffers of 64 columns
 
 // Shared memory for a row tile of N: q' (9 boxes of [N rows x 64 dims]; twice where the
 // ring keeps its five slots, so that a piece's q' loads under the one before), P ([N rows
@@ -63,6 +65,7 @@ struct Layout {
   static constexpr int kQBox = N * 128;
   static constexpr int kQBufs = N == 16 ? 2 : 1;
   static constexpr int kPBufs = N == 64 ? 1 : 2;
+  static constexpr int kOBufs = N == 64 ? 1 : 2;  // O^T accumulators: a piece's leaves under the next one's pages
   static constexpr int kSlots = N == 64 ? 4 : 5;
   static constexpr int kOffQ = 0;
   static constexpr int kOffP = kQBufs * 9 * kQBox;
@@ -75,7 +78,7 @@ struct Layout {
   static_assert((kQBufs * 9 - 1) * kQBox + 64 * 128 <= kBytes, "q' rows read outside the allocation");
   static_assert(kQBox % 1024 == 0 && kOffRope % 1024 == 0 && kOffRing % 1024 == 0, "1024-byte tiles");
   static_assert(kAlloc + 2048 <= 232448, "dynamic + static shared memory above the per-CTA limit");
-  static_assert(4 * N <= 256 && kColS + 128 <= kTmemCols, "tensor-memory regions overlap");
+  static_assert(4 * N * kOBufs <= 256 && kColS + 128 <= kTmemCols, "tensor-memory regions overlap");
 };
 constexpr int kMaxSlots = 5;
 
@@ -89,8 +92,10 @@ enum Bar {
   kSFree = kSFull + 2,         // [2] the 4 softmax warps have read them
   kPFull = kSFree + 2,         // [2] the 4 softmax warps wrote P (and rescaled O)
   kODone = kPFull + 2,         // [2] the second product of a page is done
-  kOFree = kODone + 2,         // the 4 softmax warps read O in the epilogue
-  kMeet,                       // the 4 softmax warps met
+  kOFull = kODone + 2,         // [2] the last second product of a piece is done
+  kOScale = kOFull + 2,        // [2] the 4 softmax warps wrote the piece's row factors
+  kOFree = kOScale + 2,        // [2] the 4 storing warps have read O and the factors
+  kMeet = kOFree + 2,          // the 4 softmax warps met
   kDrain,                      // [2] either issuing warp's MMAs are all done
   kNumBars = kDrain + 2
 };
@@ -182,22 +187,24 @@ __device__ __forceinline__ void store_o16(const uint32_t (&r)[16], const float* 
 }
 
 // All of a warp's O^T: four accumulators of N columns from `taddr` on, 128 dims apart, of
-// which the warp holds 32 from dim0 on; rows below `live` are stored.  The next block's
-// TMEM load flies under the current one's stores.
+// which the warp holds 32 from dim0 on; rows below `live` are stored.  Four blocks of 16
+// columns are read together.
 template <int N, bool kDirect>
 __device__ __forceinline__ void store_o(uint32_t taddr, const float* inv, int live, __nv_bfloat16* out, float* part, int dim0,
                                         int lane) {
-  constexpr int kN = 4 * (N / 16);
   const size_t at = (size_t)(lane & 3) * kDLatent + dim0 + (lane & ~3);
-  uint32_t r[2][16];
-  tmem_ld16(taddr, r[0]);
-#pragma unroll 2
-  for (int n = 0; n < kN; ++n) {
+#pragma unroll 1
+  for (int n0 = 0; n0 < 4 * (N / 16); n0 += 4) {
+    uint32_t r[4][16];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) tmem_ld16(taddr + 16 * (n0 + j), r[j]);
     tmem_wait_ld();
-    const int m = n / (N / 16), r0 = 16 * (n % (N / 16));
-    if (n + 1 < kN) tmem_ld16(taddr + 16 * (n + 1), r[(n + 1) & 1]);
-    const size_t off = at + (size_t)r0 * kDLatent + 128 * m;
-    store_o16<kDirect>(r[n & 1], inv + r0, live - r0, out + off, part + off, lane);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int n = n0 + j, m = n / (N / 16), r0 = 16 * (n % (N / 16));
+      const size_t off = at + (size_t)r0 * kDLatent + 128 * m;
+      store_o16<kDirect>(r[j], inv + r0, live - r0, out + off, part + off, lane);
+    }
   }
 }
 
@@ -214,10 +221,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ __align__(8) uint64_t bars[kNumBars];
   __shared__ uint32_t tmem_base_s;
   __shared__ int abort_s;
-  __shared__ int bad_s[8];  // [piece % 8] the piece met a page id outside the cache
+  __shared__ int bad_s[8];  // [piece % 8] 1 + the last piece that met a page id outside the cache
   __shared__ RangeScratch range_s;
-  __shared__ float al_s[2][64];   // [page parity][row] rescale factor; epilogue: 1 / l
-  __shared__ int need_s[2][4];    // [page parity][warp]
+  // Rescale factors and whether a warp has any.  Four pages deep (two with one P buffer): a
+  // warp may be that far ahead of another across the end of a piece, where they do not meet.
+  constexpr int kAhead = 2 * Lay::kPBufs;
+  __shared__ float al_s[kAhead][N];       // [page % kAhead][row]
+  __shared__ int need_s[kAhead][4];       // [page % kAhead][warp]
+  __shared__ float inv_s[Lay::kOBufs][N];  // [O buffer][row] 1 / l
 
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -243,21 +254,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(kSFree + i), 4);
       mbar_init(bar(kPFull + i), 4);
       mbar_init(bar(kODone + i), 1);
+      mbar_init(bar(kOFull + i), 1);
+      mbar_init(bar(kOScale + i), 4);
+      mbar_init(bar(kOFree + i), 4);
     }
-    mbar_init(bar(kOFree), 4);
     mbar_init(bar(kMeet), 4);
     fence_mbar_init();
     tma_prefetch_desc(&kv_map);
     tma_prefetch_desc(&rope_map);
     tma_prefetch_desc(&q_map);
   }
-  if (warp == 3) {
+  if (warp == kValues) {
     tmem_alloc(smem_u32(&tmem_base_s), kTmemCols);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  warm_params(a, tid);
   // Everything above overlaps the previous grid on the stream; from here on its writes
   // (the lengths, q', the tables, the cache) are visible.
   grid_dep_wait();
@@ -266,10 +280,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = tmem_base_s;
   const Ctl ctl{a.err, &abort_s, limit_ns};
 
-  if (warp == 0) {
+  if (warp == kLoad) {
     // ------------------------------------------------------------ page loads
-    PieceIter<kShared> pi(range_s.rg);
-    Piece pc;
+    PieceLoads<N, kShared> ld(a, range_s.rg, grp, np, lane);
     int slot = 0, piece = 0, fills = 0, g = 0;
     uint32_t phase = 1;               // parity of the "empty" phase to wait for
     uint32_t dpar = 0;                // [slot] parity of the slot's next dirty fill
@@ -277,23 +290,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t lpar = 0;                // [slot] parity of the last fill's phase
     int withheld = -1;
     bool ok = true;
-    while (ok && pi.next(pc, a)) {
-      const Task k = load_task<N, kShared>(a, pc.t, grp);
-      int ids = 0, ids_at = pc.pa - 32;  // lane l holds the id of list page ids_at + l
-      for (int p = pc.pa; p < pc.pe && ok; ++p, ++g) {
-        if (p >= ids_at + 32) {
-          ids_at = p;
-          const int pp = p + lane;
-          ids = pp < pc.pe ? (k.table ? k.table[k.s.real(pp)] : k.base + k.s.real(pp)) : 0;
-          if (__any_sync(0xffffffffu, (unsigned)ids >= (unsigned)np)) {
-            if ((unsigned)ids >= (unsigned)np) set_device_error(a.err, MLA_ERR_DEVICE_BAD_PAGE);
-            if (lane == 0) *const_cast<volatile int*>(&bad_s[piece & 7]) = 1;
-            __syncwarp();
-          }
-        }
-        const int id = __shfl_sync(0xffffffffu, ids, p - ids_at);
-        const int y = (unsigned)id < (unsigned)np ? id * kPage : np * kPage;  // out of range: reads zeros
-        const bool dirty = page_dirty(k.s, k.s.real(p));
+    while (ok && ld.next()) {
+      for (int p = ld.pc.pa; p < ld.pc.pe && ok; ++p, ++g) {
+        const int y = ld.row(p);
+        if (ld.bad && lane == 0) *const_cast<volatile int*>(&bad_s[piece & 7]) = piece + 1;
+        const bool dirty = page_dirty(ld.k.s, ld.k.s.real(p));
 #pragma unroll 1
         for (int m = 0; m < 2; ++m) {
           // The page's rope rides on its second half, whose ring slot was last held by the
@@ -324,6 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             phase ^= 1u;
           }
         }
+        if (p == ld.pc.pa) ld.look();
       }
       ++piece;
     }
@@ -334,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           drain_wait(bar((((was_dirty >> s) & 1u) ? kDirty : kFull) + s), (lpar >> s) & 1u, limit_ns);
     }
     __syncwarp();
-  } else if (warp == 1) {
+  } else if (warp == kScores) {
     // ------------------------------------------------------------ q' loads, scores
     PieceIter<kShared> pi(range_s.rg), pq(range_s.rg);  // pq: the next piece whose q' is loaded
     Piece pc, qc;
@@ -400,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int j = 1; j <= kQBufs && j <= loaded; ++j)
       drain_wait(bar(kQFull + (loaded - j) % kQBufs), ((loaded - j) / kQBufs) & 1, limit_ns);
     __syncwarp();
-  } else if (warp == 2) {
+  } else if (warp == kClean) {
     // ------------------------------------------------------------ rows in no query's sight
     PieceIter<kShared> pi(range_s.rg);
     Piece pc;
@@ -437,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-  } else if (warp == 3) {
+  } else if (warp == kValues) {
     // ------------------------------------------------------------ O^T += V^T P^T
     // An MN-major step of 16 tokens is 2048 bytes; two 64-dim boxes side by side are the
     // MN-major halves of 128 dims.
@@ -446,13 +448,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint64_t kKMajor = desc_sw128_const(16, 1024), kMNMajor = desc_sw128_const(kBox, 1024);
     const uint64_t dp = kKMajor | desc_addr(sbase + Lay::kOffP);
     const uint32_t ring = desc_addr(sbase + Lay::kOffRing);
+    constexpr int kOBufs = Lay::kOBufs;
     int slot = 0, piece = 0, g = 0;
     bool ok = true;
     while (ok && pi.next(pc, a)) {
-      const int n = pc.pe - pc.pa;
+      const int n = pc.pe - pc.pa, ob = piece % kOBufs;
+      const uint32_t o = tmem + kColO + 4 * N * ob;
       for (int i = 0; i < n; ++i, ++g) {
         if (!wait_all(bar(kPFull + (g & 1)), (g >> 1) & 1, ctl) ||
-            (i == 0 && piece > 0 && !wait_all(bar(kOFree), (piece - 1) & 1, ctl))) {
+            (i == 0 && piece >= kOBufs && !wait_all(bar(kOFree + ob), (piece / kOBufs - 1) & 1, ctl))) {
           ok = false;
           break;
         }
@@ -461,24 +465,26 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int m = 0; m < 2; ++m) {
           const uint64_t av = kMNMajor | (ring + slot * (kSlotBytes >> 4));
-          mma_x4_elect<128, 2>(tmem + kColO + N * 2 * m, av, bp, kIdescO, i ? 1u : 0u);
-          mma_x4_elect<128, 2>(tmem + kColO + N * (2 * m + 1), av + 2 * (kBox >> 4), bp, kIdescO, i ? 1u : 0u);
+          mma_x4_elect<128, 2>(o + N * 2 * m, av, bp, kIdescO, i ? 1u : 0u);
+          mma_x4_elect<128, 2>(o + N * (2 * m + 1), av + 2 * (kBox >> 4), bp, kIdescO, i ? 1u : 0u);
           mma_commit_elect(bar(kEmpty + slot));
           if (++slot == kSlots) slot = 0;
         }
         mma_commit_elect(bar(kODone + (g & 1)));
       }
+      if (!ok) break;
+      mma_commit_elect(bar(kOFull + ob));
       ++piece;
     }
     mma_commit_elect(bar(kDrain + 1));
     drain_wait(bar(kDrain + 1), 0, limit_ns);
     __syncwarp();
-  } else {
-    // ------------------------------------------------------------ softmax and epilogue
+  } else if (warp < 4) {
+    // ------------------------------------------------------------ softmax
     const int q = warp & 3;               // TMEM lane quadrant
     const int half = lane >> 4;           // which 32 of the page's 64 tokens
     const int row = 16 * q + (lane & 15); // row of the tile
-    const bool holds = 16 * q < N;        // warps beyond the tile only rescale and store O
+    const bool holds = 16 * q < N;        // warps beyond the tile only rescale O
     const uint32_t lane_addr = (uint32_t)(32 * q) << 16;
     const float scale2 = a.scale * kLog2e;
     int meets = 0;
@@ -490,15 +496,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       return r;
     };
     uint8_t* const prow = smem + Lay::kOffP + (row < N ? row : 0) * 128;
+    constexpr int kOBufs = Lay::kOBufs;
     PieceIter<kShared> pi(range_s.rg);
     Piece pc;
     int g = 0, piece = 0;
     bool ok = true;
     while (ok && pi.next(pc, a)) {
       const Task k = load_task<N, kShared>(a, pc.t, grp);
-      const int n = pc.pe - pc.pa;
-      // This row sees its task's tokens t < end with t < sinks or t >= from.
-      int end = k.s.T, from = 0;
+      const int n = pc.pe - pc.pa, ob = piece % kOBufs;
+      const uint32_t o = tmem + lane_addr + kColO + 4 * N * ob;
+      // This row sees its task's tokens t < end with t < sinks or t >= from; a row past the
+      // tile's sees none.
+      int end = -1, from = 0;
       if (row < k.live) {
         if (kShared && pc.t < a.tiles) {
           const int r = k.row0 + row, b = r / a.rows;
@@ -550,21 +559,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (need) m = m_new;
         if (i > 0) {
           // O^T's lanes are dims: a row's rescale concerns every warp.
-          if (half == 0) al_s[u][row] = alpha;
+          const int s4 = gs & (kAhead - 1);
+          if (half == 0 && holds) al_s[s4][row] = alpha;
           const bool any = __any_sync(0xffffffffu, need);
-          if (lane == 0) need_s[u][q] = any;
+          if (lane == 0) need_s[s4][q] = any;
           if (!meet()) { ok = false; break; }
-          if (need_s[u][0] | need_s[u][1] | need_s[u][2] | need_s[u][3]) {
+          if (need_s[s4][0] | need_s[s4][1] | need_s[s4][2] | need_s[s4][3]) {
             if (!wait_all(bar(kODone + (u ^ 1)), ((gs - 1) >> 1) & 1, ctl)) { ok = false; break; }
             tc_fence_after();
 #pragma unroll 1
             for (int cc = 0; cc < 4 * N; cc += 16) {
               uint32_t r[16];
-              tmem_ld16(tmem + lane_addr + kColO + cc, r);
+              tmem_ld16(o + cc, r);
               tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * al_s[u][(cc & (N - 1)) + e]);
-              tmem_st16(tmem + lane_addr + kColO + cc, r);
+              for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * al_s[s4][(cc & (N - 1)) + e]);
+              tmem_st16(o + cc, r);
             }
             tmem_wait_st();
           }
@@ -611,39 +621,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(bar(kPFull + u));
       }
       if (!ok) break;
-      // ---- epilogue: O / l in this warp's dims, lse of this warp's rows
-      const bool bad = *const_cast<volatile int*>(&bad_s[piece & 7]) != 0;
-      const int ge = g + n - 1;
+      // ---- the piece's row factors for the storing warps, and lse
+      const bool bad = *const_cast<volatile int*>(&bad_s[piece & 7]) == piece + 1;
       const float l_row = l + __shfl_xor_sync(0xffffffffu, l, 16);
       const bool none = l_row == 0.f;  // the row sees no token of the piece
-      if (!meet()) { ok = false; break; }  // every warp is done with al_s
-      if (half == 0) al_s[0][row] = bad ? NAN : (none ? 0.f : 1.f / l_row);
-      if (!meet()) { ok = false; break; }
-      if (warp == 4 && lane == 0) *const_cast<volatile int*>(&bad_s[piece & 7]) = 0;  // read by all; next used 8 pieces on
-      const bool whole = pc.pa == 0 && pc.pe == k.s.n;
-      // Rows of the partial storage (or of out) where the tile's row 0 goes.
-      size_t prow0;
-      if (whole) {
-        prow0 = kShared ? (size_t)2 * a.num_workers * N + (pc.t < a.tiles ? 0 : a.batch * a.rows) + k.row0 : k.row0;
-      } else {
-        const size_t sl = pc.t == pi.rg.b0 ? w : a.num_workers + w;
-        prow0 = (kShared ? sl : sl * a.groups + grp) * N;
-      }
-      const bool direct = whole && !kShared;
+      if (piece >= kOBufs && !wait_all(bar(kOFree + ob), (piece / kOBufs - 1) & 1, ctl)) break;
+      if (half == 0 && holds) inv_s[ob][row] = bad ? NAN : (none ? 0.f : 1.f / l_row);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kOScale + ob));
       if (holds && half == 0 && row < k.live) {
+        const PieceOut to = piece_out<N, kShared>(a, k, pc, pi.rg, w, grp);
         const float v = bad ? NAN : (none ? -INFINITY : (m + __log2f(l_row)) * kLn2);
-        (direct ? a.lse : a.part_lse)[prow0 + row] = v;
+        (to.direct ? a.lse : a.part_lse)[to.row0 + row] = v;
       }
-      if (!wait_all(bar(kODone + (ge & 1)), (ge >> 1) & 1, ctl)) { ok = false; break; }
-      tc_fence_after();
-      if (direct)
-        store_o<N, true>(tmem + lane_addr + kColO, al_s[0], k.live, a.out + prow0 * kDLatent, nullptr, 32 * q, lane);
-      else
-        store_o<N, false>(tmem + lane_addr + kColO, al_s[0], k.live, nullptr, a.part_o + prow0 * kDLatent, 32 * q, lane);
-      tc_fence_before();
-      if (!meet()) { ok = false; break; }  // al_s may be rewritten
-      if (lane == 0) mbar_arrive(bar(kOFree));
       g += n;
+      ++piece;
+    }
+  } else {
+    // ------------------------------------------------------------ O / l leaves
+    constexpr int kOBufs = Lay::kOBufs;
+    const int q = warp & 3;
+    PieceIter<kShared> pi(range_s.rg);
+    Piece pc;
+    int piece = 0;
+    while (pi.next(pc, a)) {
+      const Task k = load_task<N, kShared>(a, pc.t, grp);
+      const PieceOut to = piece_out<N, kShared>(a, k, pc, pi.rg, w, grp);
+      const int ob = piece % kOBufs, par = (piece / kOBufs) & 1;
+      const uint32_t o = tmem + ((uint32_t)(32 * q) << 16) + kColO + 4 * N * ob;
+      if (!wait_all(bar(kOScale + ob), par, ctl) || !wait_all(bar(kOFull + ob), par, ctl)) break;
+      tc_fence_after();
+      if (to.direct)
+        store_o<N, true>(o, inv_s[ob], k.live, a.out + to.row0 * kDLatent, nullptr, 32 * q, lane);
+      else
+        store_o<N, false>(o, inv_s[ob], k.live, nullptr, a.part_o + to.row0 * kDLatent, 32 * q, lane);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kOFree + ob));
       ++piece;
     }
   }
@@ -652,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) grid_dep_launch_dependents();  // the combine grid may launch (it waits for this grid's writes)
   tc_fence_before();
   __syncthreads();
-  if (warp == 3) {
+  if (warp == kValues) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }

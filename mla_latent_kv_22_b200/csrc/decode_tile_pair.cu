@@ -29,9 +29,10 @@
 // One buffer each for S and P is enough: while the softmax of step i runs, the tensor cores
 // take the values of step i - 1 and the scores of step i + 1.
 //
-// Roles (416 threads).  Warp 0: q' and score loads.  Warp 1: score MMAs (CTA 0).  Warp 2:
-// zeroes value rows that no query sees.  Warp 3: tensor memory, value MMAs (CTA 0).  Warp 4:
-// value loads.  Warps 5-12: softmax, 4 threads per row (32 tokens each), and the epilogue.
+// Roles (416 threads).  Warps 0-7: softmax, 4 threads per row (32 tokens each), and the
+// epilogue.  Warp 8: q' and score loads.  Warp 9: score MMAs (CTA 0).  Warp 10: zeroes value
+// rows that no query sees.  Warp 11: tensor memory, value MMAs (CTA 0).  Warp 12: value loads.
+// (The first warps also write the schedule's records, which the loads should not wait for.)
 // The lazy running maximum, the roundings and the bounded waits are decode_tile.cu's.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -48,7 +49,7 @@ using namespace sm100;
 
 constexpr int kRows = 128;
 constexpr int kThreads = 416;
-constexpr int kSoftmaxWarp0 = 5;
+constexpr int kLoadK = 8, kScores = 9, kClean = 10, kValues = 11, kLoadV = 12;  // warps; 0-7 are the softmax's
 constexpr int kBox = 8192;            // [64 rows x 64 bf16], 128B swizzle
 constexpr int kSlotBytes = 4 * kBox;  // a half page
 constexpr int kKSlots = 3;
@@ -142,65 +143,53 @@ __device__ __forceinline__ void arrive_cta0(uint32_t rank, uint32_t local_bar, u
   else mbar_arrive_remote(cluster_bar);
 }
 
-// The page ids of a piece, read by a warp 32 at a time.
-struct PageIds {
-  int ids, at;
-  __device__ explicit PageIds(int pa) : ids(0), at(pa - 32) {}
-  // First row of list page p; a page id outside the cache gives the row that reads zeros.
-  __device__ __forceinline__ int row(const TileArgs& a, const Task& k, const Piece& pc, int p, int np, int lane, bool* bad) {
-    if (p >= pc.pe) return np * kPage;
-    if (p >= at + 32) {
-      at = p;
-      const int pp = p + lane;
-      ids = pp < pc.pe ? (k.table ? k.table[k.s.real(pp)] : k.base + k.s.real(pp)) : 0;
-      if (__any_sync(0xffffffffu, (unsigned)ids >= (unsigned)np)) {
-        if ((unsigned)ids >= (unsigned)np) set_device_error(a.err, MLA_ERR_DEVICE_BAD_PAGE);
-        *bad = true;
-      }
-    }
-    const int id = __shfl_sync(0xffffffffu, ids, p - at);
-    return (unsigned)id < (unsigned)np ? id * kPage : np * kPage;
-  }
-};
-
 // A warp's 128 dims of its 32 rows leave through its own part of the P buffer (64 bytes of
-// 32 rows: `st` is the lane's row there, c the half of the row, h the row): 4 lanes then
-// store 64 contiguous bytes of one row.  `inv` is this lane's row's factor; `dst` is row 0
-// of the warp's 32, `live` how many of them are stored.
+// 32 rows, the c-th half of each), 16 rows of 128 bytes at a time: 8 lanes then store 128
+// contiguous bytes of one row.  `inv` is this lane's row's factor; `dst` is row 0 of the
+// warp's 32, `live` how many of them are stored.
 template <bool kDirect>
 __device__ __forceinline__ void store_rows(uint32_t taddr, float inv, uint8_t* box, int c, int r32, int lane, int live, void* dst) {
-  constexpr int kCols = kDirect ? 32 : 16;  // 64 bytes
-  const int k = lane >> 2;
-  const int sr = ((k & 1) << 2) | (k >> 1), sk = lane & 3;  // rows r and r + 4 lie in different bank halves
-  uint32_t r[kCols];
-  auto load = [&](int cc) {
-    if constexpr (kDirect) tmem_ld32(taddr + cc, r);
-    else tmem_ld16(taddr + cc, r);
+  constexpr int kCols = kDirect ? 64 : 32;  // 128 bytes
+  // The place of chunk e of staged row r: neither side meets a bank twice.
+  auto cell = [&](int r, int e) -> uint4* {
+    const int x = e ^ (r & 4), rr = (r & 3) | (x & 4) | ((r >> 2) << 3);
+    return reinterpret_cast<uint4*>(box + (r32 + rr) * 128 + (((4 * c + (x & 3)) ^ (rr & 7)) * 16));
   };
-  load(0);
 #pragma unroll 1
   for (int cc = 0; cc < 128; cc += kCols) {
-    uint32_t w[16];
-    tmem_wait_ld();
+    uint32_t w[32];
+    if constexpr (kDirect) {
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      if constexpr (kDirect) w[e] = pack_bf16x2(__uint_as_float(r[2 * e]) * inv, __uint_as_float(r[2 * e + 1]) * inv);
-      else w[e] = __float_as_uint(__uint_as_float(r[e]) * inv);
+      for (int j = 0; j < 2; ++j) {
+        uint32_t r[32];
+        tmem_ld32(taddr + cc + 32 * j, r);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          w[16 * j + e] = pack_bf16x2(__uint_as_float(r[2 * e]) * inv, __uint_as_float(r[2 * e + 1]) * inv);
+      }
+    } else {
+      tmem_ld32(taddr + cc, w);
+      tmem_wait_ld();
+#pragma unroll
+      for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * inv);
     }
-    if (cc + kCols < 128) load(cc + kCols);  // flies under the stores
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      *reinterpret_cast<uint4*>(box + (r32 + lane) * 128 + (((4 * c + e) ^ (lane & 7)) * 16)) =
-          make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
-    __syncwarp();
+    for (int half = 0; half < 2; ++half) {
+      if (lane >> 4 == half) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int rr = 8 * i + sr;
-      const uint4 v = *reinterpret_cast<const uint4*>(box + (r32 + rr) * 128 + (((4 * c + sk) ^ (rr & 7)) * 16));
-      if (rr < live)
-        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(dst) + ((size_t)rr * kDLatent + cc) * (kDirect ? 2 : 4) + sk * 16) = v;
+        for (int e = 0; e < 8; ++e) *cell(lane & 15, e) = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+      }
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 4 * i + (lane >> 3), row = 16 * half + r;
+        const uint4 v = *cell(r, lane & 7);
+        if (row < live)
+          *reinterpret_cast<uint4*>(static_cast<uint8_t*>(dst) + ((size_t)row * kDLatent + cc) * (kDirect ? 2 : 4) + (lane & 7) * 16) = v;
+      }
+      __syncwarp();  // the staging area is rewritten by the next rows
     }
-    __syncwarp();  // the staging area is rewritten by the next columns
   }
 }
 
@@ -213,7 +202,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __shared__ __align__(8) uint64_t bars[kNumBars];
   __shared__ uint32_t tmem_base_s;
   __shared__ int abort_s;
-  __shared__ int bad_s[8];  // [piece % 8] the piece met a page id outside the cache
+  __shared__ int bad_s[8];  // [piece % 8] 1 + the last piece that met a page id outside the cache
   __shared__ RangeScratch range_s;
   __shared__ float mx_s[2][2][2][64];  // [step parity][page][column half][row]
   __shared__ float lsum_s[2][2][64];   // [page][column half][row]
@@ -256,7 +245,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&rope_map);
     tma_prefetch_desc(&q_map);
   }
-  if (warp == 3) {
+  if (warp == kValues) {
     tmem_alloc_pair(smem_u32(&tmem_base_s), kTmemCols);
     tmem_relinquish_pair();
   }
@@ -264,6 +253,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncthreads();
   cluster_sync();  // barriers and tensor memory of both CTAs ready before any remote access
   tc_fence_after();
+  warm_params(a, tid);
   // Everything above overlaps the previous grid on the stream; from here on its writes
   // (the lengths, q', the tables, the cache) are visible.
   grid_dep_wait();
@@ -273,22 +263,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const Ctl ctl{a.err, &abort_s, map_to_rank(smem_u32(&abort_s), rank ^ 1u), limit_ns};
   auto bar0 = [&](int i) { return map_to_rank(bar(i), 0); };
 
-  if (warp == 0) {
+  if (warp == kLoadK) {
     // ------------------------------------------------------------ q' and score loads
-    PieceIter<kShared> pi(range_s.rg);
-    Piece pc;
+    PieceLoads<kRows, kShared> ld(a, range_s.rg, grp, np, lane);  // bad pages: the value loads report them
     int slot = 0, piece = 0, fills = 0, g = 0;
     uint32_t phase = 1;
     int withheld = -1;
     bool ok = true;
-    while (ok && pi.next(pc, a)) {
-      const Task k = load_task<kRows, kShared>(a, pc.t, grp);
-      const int steps = (pc.pe - pc.pa + 1) / 2;
-      PageIds ids(pc.pa);
-      bool bad = false;  // the value loads report it
+    while (ok && ld.next()) {
+      const int steps = (ld.pc.pe - ld.pc.pa + 1) / 2;
       // q' dims [0, 384) pass through two score slots on their way to tensor memory, so that
       // they are here before the tensor memory is free; the rest needs its place free first.
-      const int qrow = k.row0 + 64 * (int)rank;
+      const int qrow = ld.k.row0 + 64 * (int)rank;
       for (int m = 0; m < 2; ++m) {
         if (!wait_all(bar(kEmptyK + slot), phase, ctl)) { ok = false; break; }
         if (lane == 0) {
@@ -308,7 +294,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tma_load_3d_pair(sbase + kOffQ, &q_map, 0, qrow, kQTmemBoxes, bar0(kQFull));
       }
       for (int i = 0; i < steps && ok; ++i, ++g) {
-        const int y = ids.row(a, k, pc, pc.pa + 2 * i + (int)rank, np, lane, &bad);
+        const int y = ld.row(ld.pc.pa + 2 * i + (int)rank);
 #pragma unroll 1
         for (int m = 0; m < 2; ++m) {
           // The rope rides on the second half.  That half's slot was last held by the first
@@ -328,6 +314,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             phase ^= 1u;
           }
         }
+        if (i == 0) ld.look();
       }
       ++piece;
     }
@@ -341,27 +328,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (piece > 0) drain_wait(bar(kQFull), (piece - 1) & 1, limit_ns);
     }
     __syncwarp();
-  } else if (warp == 4) {
+  } else if (warp == kLoadV) {
     // ------------------------------------------------------------ value loads
-    PieceIter<kShared> pi(range_s.rg);
-    Piece pc;
+    PieceLoads<kRows, kShared> ld(a, range_s.rg, grp, np, lane);
     int piece = 0, g = 0;
     uint32_t dirty_fills[2] = {0, 0};
     bool ok = true;
-    while (ok && pi.next(pc, a)) {
-      const Task k = load_task<kRows, kShared>(a, pc.t, grp);
-      const int steps = (pc.pe - pc.pa + 1) / 2;
-      PageIds ids(pc.pa);
-      bool bad = false;
+    while (ok && ld.next()) {
+      const int steps = (ld.pc.pe - ld.pc.pa + 1) / 2;
       for (int i = 0; i < steps && ok; ++i, ++g) {
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
-          const int p = pc.pa + 2 * i + m;
-          const int y = ids.row(a, k, pc, p, np, lane, &bad);
-          const bool dirty = p < pc.pe && page_dirty(k.s, k.s.real(p));
+          const int p = ld.pc.pa + 2 * i + m;
+          const int y = ld.row(p);
+          const bool dirty = p < ld.pc.pe && page_dirty(ld.k.s, ld.k.s.real(p));
           if (!wait_all(bar(kEmptyV + m), (g & 1) ^ 1, ctl)) { ok = false; break; }
           if (lane == 0) {
-            if (bad) *const_cast<volatile int*>(&bad_s[piece & 7]) = 1;
+            if (ld.bad) *const_cast<volatile int*>(&bad_s[piece & 7]) = piece + 1;
             const uint32_t dst = sbase + kOffV + m * kSlotBytes;
             if (dirty) {
               mbar_expect_tx(bar(kDirty + m), kSlotBytes);
@@ -376,6 +359,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           dirty_fills[m] += dirty ? 1u : 0u;
         }
+        if (i == 0) ld.look();
       }
       ++piece;
     }
@@ -385,7 +369,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (ok && g > 0 && rank == 0) drain_wait(bar(kFullV + m), (g - 1) & 1, limit_ns);
     }
     __syncwarp();
-  } else if (warp == 1) {
+  } else if (warp == kScores) {
     // ------------------------------------------------------------ score MMAs
     if (rank == 0) {
       PieceIter<kShared> pi(range_s.rg);
@@ -443,7 +427,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       drain_wait(bar(kDrain), 0, limit_ns);
     }
     __syncwarp();
-  } else if (warp == 3) {
+  } else if (warp == kValues) {
     // ------------------------------------------------------------ value MMAs
     if (rank == 0) {
       PieceIter<kShared> pi(range_s.rg);
@@ -478,7 +462,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       drain_wait(bar(kDrain + 1), 0, limit_ns);
     }
     __syncwarp();
-  } else if (warp == 2) {
+  } else if (warp == kClean) {
     // ------------------------------------------------------------ value rows in no query's sight
     PieceIter<kShared> pi(range_s.rg);
     Piece pc;
@@ -511,7 +495,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else {
     // ------------------------------------------------------------ softmax and epilogue
     const int q = warp & 3;                     // TMEM lane quadrant
-    const int c = (warp - kSoftmaxWarp0) >> 2;  // which 32 of a page's 64 tokens, and O block
+    const int c = warp >> 2;  // which 32 of a page's 64 tokens, and O block
     const int h = (32 * q + lane) & 63;         // row within this CTA
     const int hh = q >> 1;                      // page of the step held in this lane
     const int row = 64 * (int)rank + h;         // row of the tile
@@ -691,26 +675,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const float l_row = (lsum_s[0][0][h] + lsum_s[0][1][h]) + (lsum_s[1][0][h] + lsum_s[1][1][h]);
       if (!wait_all(bar(kODone), ge & 1, ctl)) { ok = false; break; }
       tc_fence_after();
-      const bool bad = *const_cast<volatile int*>(&bad_s[piece & 7]) != 0;
+      const bool bad = *const_cast<volatile int*>(&bad_s[piece & 7]) == piece + 1;
       const bool none = l_row == 0.f;  // the row sees no token of the piece
       const float inv = bad ? NAN : (none ? 0.f : 1.f / l_row);
-      const bool whole = pc.pa == 0 && pc.pe == k.t.s.n;
-      // Rows of the partial storage (or of out) where the tile's row 0 goes.
-      size_t prow0;
-      if (whole) {
-        prow0 = kShared ? (size_t)2 * a.num_workers * kRows + (pc.t < a.tiles ? 0 : a.batch * a.rows) + k.t.row0 : k.t.row0;
-      } else {
-        const size_t sl = pc.t == pi.rg.b0 ? w : a.num_workers + w;
-        prow0 = (kShared ? sl : sl * a.groups + grp) * kRows;
-      }
-      const bool direct = whole && !kShared;
+      const PieceOut to = piece_out<kRows, kShared>(a, k.t, pc, pi.rg, w, grp);
       if (hh == 0 && c == 0 && row < k.t.live) {
         const float v = bad ? NAN : (none ? -INFINITY : (m + __log2f(l_row)) * kLn2);
-        (direct ? a.lse : a.part_lse)[prow0 + row] = v;
+        (to.direct ? a.lse : a.part_lse)[to.row0 + row] = v;
       }
-      const size_t at = (prow0 + 64 * rank + r32) * kDLatent + 256 * hh + 128 * c;
+      const size_t at = (to.row0 + 64 * rank + r32) * kDLatent + 256 * hh + 128 * c;
       const int live = k.t.live - 64 * (int)rank - r32;
-      if (direct)
+      if (to.direct)
         store_rows<true>(tmem + lane_addr + kColO + 128 * c, inv, pbox, c, r32, lane, live, a.out + at);
       else
         store_rows<false>(tmem + lane_addr + kColO + 128 * c, inv, pbox, c, r32, lane, live, a.part_o + at);
@@ -733,7 +708,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   }
   cluster_sync();  // the peer's MMAs, loads and arrivals are done with this CTA
-  if (warp == 3) {
+  if (warp == kValues) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, kTmemCols);
   }

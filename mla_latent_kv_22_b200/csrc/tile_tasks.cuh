@@ -13,6 +13,14 @@
 
 namespace mla {
 
+// Brings a launch's parameters into the constant cache while the previous grid ends.
+__device__ __forceinline__ void warm_params(const TileArgs& a, int tid) {
+  if (tid < (int)(sizeof(TileArgs) / 4)) {
+    const int v = reinterpret_cast<const int*>(&a)[tid];
+    asm volatile("" ::"r"(v));
+  }
+}
+
 // ---------------------------------------------------------------- tasks
 // The pages of a task: page p of its list is page real(p) of its table; the first `ns`
 // hold the sinks, the rest run from the window's first page to the last.
@@ -110,6 +118,82 @@ struct PieceIter {
       }
     }
     return false;
+  }
+};
+
+// Where a piece's results go: out / lse (direct), or a partial's storage; row0 is the row of
+// either that the tile's row 0 takes.
+struct PieceOut {
+  bool direct;
+  size_t row0;
+};
+
+template <int N, bool kShared>
+__device__ __forceinline__ PieceOut piece_out(const TileArgs& a, const Task& k, const Piece& pc, const WorkerRange& rg, int w,
+                                              int grp) {
+  if (pc.pa == 0 && pc.pe == k.s.n) {
+    if (!kShared) return {true, (size_t)k.row0};
+    return {false, (size_t)2 * a.num_workers * N + (pc.t < a.tiles ? 0 : a.batch * a.rows) + k.row0};
+  }
+  const size_t slot = pc.t == rg.b0 ? w : a.num_workers + w;
+  return {false, (kShared ? slot : slot * a.groups + grp) * N};
+}
+
+// A loading warp's walk over its worker's pages.  The next piece's task and first page ids
+// are read (look) while the current piece loads, so that a piece starts without waiting for
+// its table.
+template <int N, bool kShared>
+struct PieceLoads {
+  const TileArgs& a;
+  const int grp, np, lane;
+  PieceIter<kShared> it;
+  Piece pc, nc;
+  Task k, nk;
+  int ids, nids, at;  // lane l holds the id of list page at + l
+  bool have, fresh, bad;
+
+  __device__ PieceLoads(const TileArgs& args, const volatile WorkerRange& rg, int g, int num_pages, int l)
+      : a(args), grp(g), np(num_pages), lane(l), it(rg) {
+    look();
+  }
+  __device__ __forceinline__ int id(const Task& t, const Piece& p, int pp) const {
+    return pp < p.pe ? (t.table ? t.table[t.s.real(pp)] : t.base + t.s.real(pp)) : 0;
+  }
+  __device__ __forceinline__ void look() {
+    have = it.next(nc, a);
+    if (!have) return;
+    nk = load_task<N, kShared>(a, nc.t, grp);
+    nids = id(nk, nc, nc.pa + lane);
+  }
+  // The piece looked up last becomes the current one.
+  __device__ __forceinline__ bool next() {
+    if (!have) return false;
+    pc = nc;
+    k = nk;
+    ids = nids;
+    at = pc.pa;
+    fresh = true;
+    bad = have = false;
+    return true;
+  }
+  // First row of list page p; a page id outside the cache gives the row that reads zeros,
+  // the error, and `bad` for the rest of the piece.
+  __device__ __forceinline__ int row(int p) {
+    if (p >= pc.pe) return np * kPage;
+    if (p >= at + 32) {
+      at = p;
+      ids = id(k, pc, p + lane);
+      fresh = true;
+    }
+    if (fresh) {
+      fresh = false;
+      if (__any_sync(0xffffffffu, (unsigned)ids >= (unsigned)np)) {
+        if ((unsigned)ids >= (unsigned)np) set_device_error(a.err, MLA_ERR_DEVICE_BAD_PAGE);
+        bad = true;
+      }
+    }
+    const int v = __shfl_sync(0xffffffffu, ids, p - at);
+    return (unsigned)v < (unsigned)np ? v * kPage : np * kPage;
   }
 };
 
