@@ -521,7 +521,7 @@ mla_status_t tile_call(TileArgs& a, void* workspace, size_t workspace_bytes, mla
   tile_schedule(&a);
   // The schedule's units (pages, and a fixed cost per task) are counted in 32 bits.
   const long long units = shared ? (long long)a.tiles * ((long long)a.prefix_blocks + kMaxPieceCost) +
-                                       (long long)a.batch * a.groups * ((long long)a.max_blocks + kMaxPieceCost)
+                                       ((long long)a.tiles + a.batch) * (long long)a.max_blocks
                                  : (long long)a.batch * ((long long)a.max_blocks + kMaxPieceCost);
   if (units > (1LL << 31) - 1) return fail(MLA_ERR_UNSUPPORTED, "batch too large for the 32-bit split schedule");
   a.err = d->err;

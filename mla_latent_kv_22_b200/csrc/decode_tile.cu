@@ -106,37 +106,35 @@ __device__ __forceinline__ uint64_t now_ns() {
   return t;
 }
 
+// What a wait needs besides its barrier, in shared memory: few registers across the kernel.
 struct Ctl {
   int* err;
-  volatile int* abort;
   uint64_t limit_ns;
+  int abort;
 };
 
-__device__ __noinline__ void wait_timed_out(int* err, volatile int* abort) {
-  set_device_error(err, MLA_ERR_DEVICE_TIMEOUT);
-  *abort = 1;
-}
-
-// Bounded wait on an mbarrier phase; false on timeout (recorded) or abort.
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const Ctl& c) {
-  if (mbar_try_wait_cta(bar, parity)) return true;
+// Bounded wait on an mbarrier phase; false on timeout (recorded) or abort.  The first try is
+// inlined, the rest is not (it would be at some thirty places).
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, Ctl* c) {
   uint64_t t0 = 0;
+#pragma unroll 1
   for (uint32_t i = 1;; ++i) {
     if (mbar_try_wait_cta(bar, parity)) return true;
     if ((i & 63) == 0) {
-      if (*c.abort) return false;
+      if (*const_cast<volatile int*>(&c->abort)) return false;
       const uint64_t t = now_ns();
       if (t0 == 0) {
         t0 = t;
-      } else if (t - t0 > c.limit_ns) {
-        wait_timed_out(c.err, c.abort);
+      } else if (t - t0 > c->limit_ns) {
+        set_device_error(c->err, MLA_ERR_DEVICE_TIMEOUT);
+        *const_cast<volatile int*>(&c->abort) = 1;
         return false;
       }
     }
   }
 }
-__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, const Ctl& c) {
-  return __all_sync(0xffffffffu, wait_bar(bar, parity, c));
+__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, Ctl* c) {
+  return __all_sync(0xffffffffu, mbar_try_wait_cta(bar, parity) || wait_long(bar, parity, c));
 }
 __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
   const uint64_t t0 = now_ns();
@@ -220,8 +218,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[kNumBars];
   __shared__ uint32_t tmem_base_s;
-  __shared__ int abort_s;
-  __shared__ int bad_s[8];  // [piece % 8] 1 + the last piece that met a page id outside the cache
+  __shared__ Ctl ctl_s;
+  constexpr int kWords = (N + 31) / 32;
+  __shared__ uint32_t bad_s[8][kWords];  // [piece % 8] a bit for each row that a page id outside the cache spoils
   __shared__ RangeScratch range_s;
   // Rescale factors and whether a warp has any.  Four pages deep (two with one P buffer): a
   // warp may be that far ahead of another across the end of a piece, where they do not meet.
@@ -239,8 +238,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int np = a.block_table ? a.num_pages : a.batch * a.max_blocks;
 
   if (tid == 0) {
-    abort_s = 0;
-    for (int i = 0; i < 8; ++i) bad_s[i] = 0;
+    ctl_s = Ctl{a.err, limit_ns, 0};
+    for (int i = 0; i < 8 * kWords; ++i) bad_s[i / kWords][i % kWords] = 0;
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(bar(kFull + s), 1);   // the producer, or the cleaning warp
       mbar_init(bar(kEmpty + s), 1);  // MMA commit
@@ -275,10 +274,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Everything above overlaps the previous grid on the stream; from here on its writes
   // (the lengths, q', the tables, the cache) are visible.
   grid_dep_wait();
-  derive_range(TaskLengths<kShared>{&a}, kShared ? a.tiles + a.batch * a.groups : a.batch, a.num_workers, a.min_pages,
+  derive_range(TaskLengths<kShared>{&a}, kShared ? a.tiles : a.batch, a.num_workers, a.min_pages,
                a.granule, a.whole_slack, a.piece_cost, a.task, a.err, w, range_s);
   const uint32_t tmem = tmem_base_s;
-  const Ctl ctl{a.err, &abort_s, limit_ns};
+  Ctl* const ctl = &ctl_s;
 
   if (warp == kLoad) {
     // ------------------------------------------------------------ page loads
@@ -291,10 +290,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     int withheld = -1;
     bool ok = true;
     while (ok && ld.next()) {
+      // The marks four pieces on are those of four pieces back: read, since these loads run
+      // less than four pieces ahead of the softmax (at most five halves of pages).
+      if (lane < kWords) bad_s[(piece + 4) & 7][lane] = 0;
+      __syncwarp();
       for (int p = ld.pc.pa; p < ld.pc.pe && ok; ++p, ++g) {
-        const int y = ld.row(p);
-        if (ld.bad && lane == 0) *const_cast<volatile int*>(&bad_s[piece & 7]) = piece + 1;
-        const bool dirty = page_dirty(ld.k.s, ld.k.s.real(p));
+        bool dirty;
+        const int y = ld.row(p, dirty, bad_s[piece & 7]);
 #pragma unroll 1
         for (int m = 0; m < 2; ++m) {
           // The page's rope rides on its second half, whose ring slot was last held by the
@@ -411,32 +413,38 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     while (ok && pi.next(pc, a)) {
       const Task k = load_task<N, kShared>(a, pc.t, grp);
-      for (int p = pc.pa; p < pc.pe && ok; ++p) {
-        const int real = k.s.real(p), t0 = real * kPage;
-        if (!page_dirty(k.s, real)) {
-          slot += 2;
-          if (slot >= kSlots) slot -= kSlots;
-          continue;
-        }
-        // Rows [h0, h1) and [e0, 64) of the page.
-        const int h0 = max(k.s.hole0 - t0, 0), h1 = max(h0, min(k.s.hole1 - t0, kPage));
-        const int e0 = min(max(k.s.T - t0, 0), kPage);
-        const int nrow = (h1 - h0) + (kPage - e0);
-        for (int m = 0; m < 2; ++m) {
-          if (!wait_all(bar(kDirty + slot), (dpar >> slot) & 1u, ctl)) { ok = false; break; }
-          dpar ^= 1u << slot;
-          uint8_t* st = smem + Lay::kOffRing + slot * kSlotBytes;
-          for (int idx = lane; idx < nrow * 8; idx += 32) {
-            const int r = idx / 8, row = r < h1 - h0 ? h0 + r : e0 + (r - (h1 - h0));
+      for (int p0 = pc.pa; p0 < pc.pe && ok; p0 += 32) {
+        const int np0 = min(32, pc.pe - p0);
+        const PageRef ref = page_ref<kShared>(a, k, min(p0 + lane, pc.pe - 1));
+        uint32_t dirty = __ballot_sync(0xffffffffu, lane < np0 && page_dirty<kShared>(k, ref));
+        int done = 0;  // pages of the 32 passed
+        for (; dirty && ok; dirty &= dirty - 1) {
+          const int j = __ffs(dirty) - 1;
+          slot = (slot + 2 * (j - done)) % kSlots;
+          done = j + 1;
+          const int t0 = __shfl_sync(0xffffffffu, ref.page, j) * kPage;
+          // Rows [h0, h1) and [e0, 64) of the page.
+          const int h0 = kShared ? 0 : max(k.s.hole0 - t0, 0), h1 = kShared ? 0 : max(h0, min(k.s.hole1 - t0, kPage));
+          const int e0 = __shfl_sync(0xffffffffu, ref.valid_rows(), j);
+          const int nrow = (h1 - h0) + (kPage - e0);
+          for (int m = 0; m < 2; ++m) {
+            if (!wait_all(bar(kDirty + slot), (dpar >> slot) & 1u, ctl)) { ok = false; break; }
+            dpar ^= 1u << slot;
+            uint8_t* st = smem + Lay::kOffRing + slot * kSlotBytes;
+#pragma unroll 1
+            for (int idx = lane; idx < nrow * 8; idx += 32) {
+              const int r = idx / 8, row = r < h1 - h0 ? h0 + r : e0 + (r - (h1 - h0));
 #pragma unroll
-            for (int box = 0; box < 4; ++box)
-              *reinterpret_cast<uint4*>(st + box * kBox + row * 128 + (idx % 8) * 16) = make_uint4(0, 0, 0, 0);
+              for (int box = 0; box < 4; ++box)
+                *reinterpret_cast<uint4*>(st + box * kBox + row * 128 + (idx % 8) * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kFull + slot));
+            if (++slot == kSlots) slot = 0;
           }
-          fence_proxy_async();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(kFull + slot));
-          if (++slot == kSlots) slot = 0;
         }
+        slot = (slot + 2 * (np0 - done)) % kSlots;
       }
     }
   } else if (warp == kValues) {
@@ -505,21 +513,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Task k = load_task<N, kShared>(a, pc.t, grp);
       const int n = pc.pe - pc.pa, ob = piece % kOBufs;
       const uint32_t o = tmem + lane_addr + kColO + 4 * N * ob;
-      // This row sees its task's tokens t < end with t < sinks or t >= from; a row past the
-      // tile's sees none.
-      int end = -1, from = 0;
-      if (row < k.live) {
-        if (kShared && pc.t < a.tiles) {
-          const int r = k.row0 + row, b = r / a.rows;
-          end = min(k.s.T, k.s.T + a.seqlens[b] - a.s_q + 1 + (r - b * a.rows) / a.heads);
-        } else {
-          end = k.s.T - a.s_q + 1 + (k.srow + row) / a.heads;
-          if (!kShared) from = end - a.window;
-        }
-      }
+      const RowSight sight = row_sight<kShared>(a, k, row);
+      PageRef ref{};  // lane l: list page pa + 32 (i / 32) + l
       float m = -INFINITY, l = 0.f;
       for (int i = 0; i < n && ok; ++i) {
         const int gs = g + i, u = gs & 1;
+        if ((i & 31) == 0) ref = page_ref<kShared>(a, k, min(pc.pa + i + lane, pc.pe - 1));
         float y[32];
         float mp = -INFINITY;
         if (!wait_all(bar(kSFull + u), (gs >> 1) & 1, ctl)) { ok = false; break; }
@@ -535,9 +534,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kSFree + u));
         if (holds) {
-          const int t0 = k.s.real(pc.pa + i) * kPage + 32 * half;
-          uint32_t see = below(end - t0);
-          if (!kShared) see &= below(a.sinks - t0) | ~below(from - t0);
+          const int t0 = __shfl_sync(0xffffffffu, ref.page, i & 31) * kPage + 32 * half;
+          uint32_t see;
+          if constexpr (kShared) {
+            const int seq = __shfl_sync(0xffffffffu, ref.seq, i & 31);
+            see = seq < 0 ? below(sight.prefix_end - t0) : seq == sight.seq ? below(sight.end - t0) : 0u;
+          } else {
+            see = below(sight.end - t0) & (below(a.sinks - t0) | ~below(sight.from - t0));
+          }
           const uint64_t s2 = f2_pack(scale2, scale2);
 #pragma unroll
           for (int j = 0; j < 32; j += 2) f2_unpack(f2_mul(f2_pack(y[j], y[j + 1]), s2), y[j], y[j + 1]);
@@ -622,7 +626,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       // ---- the piece's row factors for the storing warps, and lse
-      const bool bad = *const_cast<volatile int*>(&bad_s[piece & 7]) == piece + 1;
+      const bool bad =
+          sight.bad || (holds && ((const_cast<volatile uint32_t&>(bad_s[piece & 7][row >> 5]) >> (row & 31)) & 1u));
       const float l_row = l + __shfl_xor_sync(0xffffffffu, l, 16);
       const bool none = l_row == 0.f;  // the row sees no token of the piece
       if (piece >= kOBufs && !wait_all(bar(kOFree + ob), (piece / kOBufs - 1) & 1, ctl)) break;
@@ -673,93 +678,79 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------- combine
-// One warp per query row: merges the pieces of its task (window), or of its rows against
-// the prefix and against the sequence's own tokens, by their lse, in that fixed order.
-constexpr int kCombineWarps = 4;
+// Merges the pieces of a row's task by their lse, in the order of their pages, and writes the
+// rows that no piece holds.  Four warps take a row, 128 dims each, and four pieces' loads are
+// in flight at a time, the first four before the weights are known (7 rows of 9 pieces ran
+// 4.5 us from serial loads).
+constexpr int kCombineThreads = 256, kCombineRows = kCombineThreads / 128, kCombineCtas = 6;  // per SM
 
 template <bool kShared>
-__global__ void __launch_bounds__(kCombineWarps * 32) combine_tile_kernel(const __grid_constant__ TileArgs a) {
+__global__ void __launch_bounds__(kCombineThreads, kCombineCtas) combine_tile_kernel(const __grid_constant__ TileArgs a) {
   grid_dep_launch_dependents();
   grid_dep_wait();
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, part = (threadIdx.x >> 5) & 3;
   const int R = a.batch * a.rows, N = a.row_tile;
-  const int gr = blockIdx.x * kCombineWarps + (threadIdx.x >> 5);
-  if (gr >= R) return;
-  const int b = gr / a.rows, r = gr - b * a.rows, g = r / N, rr = r % N;
-  SeqInfo s0, s1;
-  int r0, r1;  // the row within its tile, for either task
-  if (kShared) {
-    s0 = a.task[gr / N];
-    r0 = gr % N;
-    s1 = a.task[a.tiles + b * a.groups + g];
-    r1 = rr;
-  } else {
-    s0 = a.task[b];
-    if (s0.num_pieces == 1) return;  // written by the decode grid
-    s1 = SeqInfo{0, 0, 0};
-    r0 = g * N + rr;
-    r1 = 0;
-  }
-  uint4* out4 = reinterpret_cast<uint4*>(a.out + (size_t)gr * kDLatent);  // lane: dims 8 lane .. and 256 + 8 lane ..
-  const bool bad = s0.num_pieces < 0 || s1.num_pieces < 0;
-  const int n0 = max(s0.num_pieces, 0), n = n0 + max(s1.num_pieces, 0);
-  // Storage row of piece k.
-  auto at = [&](int k) -> size_t {
-    const bool own = k >= n0;
-    const SeqInfo& s = own ? s1 : s0;
-    const int j = own ? k - n0 : k;
-    if (kShared && s.num_pieces == 1) return (size_t)2 * a.num_workers * N + (own ? R : 0) + gr;
-    const size_t slot = j == 0 ? s.first_slot : s.first_worker + j;
-    return kShared ? slot * N + (own ? r1 : r0) : slot * a.groups * N + r0;
-  };
-  const float lk = lane < n ? a.part_lse[at(lane)] : -INFINITY;
-  float L = lk;
-  bool nan = lk != lk;
-  for (int k = lane + 32; k < n; k += 32) {
-    const float v = a.part_lse[at(k)];
-    nan |= v != v;
-    L = fmaxf(L, v);
-  }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) L = fmaxf(L, __shfl_xor_sync(0xffffffffu, L, o));
-  if (bad || __any_sync(0xffffffffu, nan) || L == -INFINITY) {
-    const bool isnan = bad || __any_sync(0xffffffffu, nan);
-    const uint32_t v = isnan ? 0x7fff7fffu : 0u;
-    out4[lane] = make_uint4(v, v, v, v);
-    out4[lane + 32] = make_uint4(v, v, v, v);
-    if (lane == 0) a.lse[gr] = isnan ? NAN : -INFINITY;
-    return;
-  }
-  float acc[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-  float wsum = 0.f;
-#pragma unroll 2
-  for (int k = 0; k < n; ++k) {
-    const size_t row = at(k);
-    const float wk = expf((k < 32 ? __shfl_sync(0xffffffffu, lk, k) : a.part_lse[row]) - L);
-    wsum += wk;
-    const float4* src = reinterpret_cast<const float4*>(a.part_o + row * kDLatent);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float4 x = src[64 * h + 2 * lane], z = src[64 * h + 2 * lane + 1];
-      acc[8 * h + 0] += wk * x.x;
-      acc[8 * h + 1] += wk * x.y;
-      acc[8 * h + 2] += wk * x.z;
-      acc[8 * h + 3] += wk * x.w;
-      acc[8 * h + 4] += wk * z.x;
-      acc[8 * h + 5] += wk * z.y;
-      acc[8 * h + 6] += wk * z.z;
-      acc[8 * h + 7] += wk * z.w;
+#pragma unroll 1
+  for (int gr = blockIdx.x * kCombineRows + (threadIdx.x >> 7); gr < R; gr += gridDim.x * kCombineRows) {
+    const int b = gr / a.rows, r = gr - b * a.rows;
+    const SeqInfo s = a.task[kShared ? gr / N : b];
+    bool nan = s.num_pieces < 0;
+    if (kShared && bad_length(a.seqlens[b], a.max_blocks)) {
+      set_device_error(a.err, MLA_ERR_DEVICE_BAD_PAGE);
+      nan = true;
     }
-  }
-  const float inv = 1.f / wsum;
+    if (s.num_pieces == 1) continue;  // written by the decode grid
+    const int n = max(s.num_pieces, 0);
+    // Storage row of piece k; a window's groups lie side by side, N rows each.
+    const size_t stride = kShared ? N : (size_t)a.groups * N;
+    const int r0 = kShared ? gr % N : r;
+    auto at = [&](int k) -> size_t { return (size_t)(k == 0 ? s.first_slot : s.first_worker + k) * stride + r0; };
+    float4 x[4];
+    auto load = [&](int k0) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
-    out4[32 * h + lane] =
-        make_uint4(pack_bf16x2(acc[8 * h] * inv, acc[8 * h + 1] * inv), pack_bf16x2(acc[8 * h + 2] * inv, acc[8 * h + 3] * inv),
-                   pack_bf16x2(acc[8 * h + 4] * inv, acc[8 * h + 5] * inv), pack_bf16x2(acc[8 * h + 6] * inv, acc[8 * h + 7] * inv));
-  if (lane == 0) a.lse[gr] = L + logf(wsum);
+      for (int j = 0; j < 4; ++j)
+        x[j] = k0 + j < n ? reinterpret_cast<const float4*>(a.part_o + at(k0 + j) * kDLatent)[32 * part + lane]
+                          : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    load(0);
+    float mine = lane < n ? a.part_lse[at(lane)] : -INFINITY, L = mine;  // piece lane's, later its weight
+    nan |= mine != mine;
+#pragma unroll 1
+    for (int k = lane + 32; k < n; k += 32) {
+      const float v = a.part_lse[at(k)];
+      nan |= v != v;
+      L = fmaxf(L, v);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) L = fmaxf(L, __shfl_xor_sync(0xffffffffu, L, o));
+    uint2* const out2 = reinterpret_cast<uint2*>(a.out + (size_t)gr * kDLatent) + 32 * part + lane;
+    nan = __any_sync(0xffffffffu, nan);
+    if (nan || L == -INFINITY) {
+      const uint32_t v = nan ? 0x7fff7fffu : 0u;
+      *out2 = make_uint2(v, v);
+      if (part == 0 && lane == 0) a.lse[gr] = nan ? NAN : -INFINITY;
+      continue;
+    }
+    mine = expf(mine - L);
+    float acc[4] = {0.f, 0.f, 0.f, 0.f}, wsum = 0.f;
+#pragma unroll 1
+    for (int k0 = 0; k0 < n; k0 += 4) {
+      if (k0) load(k0);
+      if (k0 && (k0 & 31) == 0) mine = k0 + lane < n ? expf(a.part_lse[at(k0 + lane)] - L) : 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float wk = __shfl_sync(0xffffffffu, mine, (k0 + j) & 31);  // 0 past the last piece
+        wsum += wk;
+        acc[0] += wk * x[j].x;
+        acc[1] += wk * x[j].y;
+        acc[2] += wk * x[j].z;
+        acc[3] += wk * x[j].w;
+      }
+    }
+    const float inv = 1.f / wsum;
+    *out2 = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+    if (part == 0 && lane == 0) a.lse[gr] = L + logf(wsum);
+  }
 }
 
 template <int N, bool kShared>
@@ -777,6 +768,7 @@ cudaError_t launch_tile(const TileArgs& a, cudaStream_t stream) {
 }  // namespace
 
 size_t plan_tile(TileArgs* a, int sm_count, int forced_workers, void* base) {
+  a->sm_count = sm_count;
   const bool shared = a->prefix_len != nullptr;
   const long long R = (long long)a->batch * a->rows;
   // Up to 64 rows, the narrowest tile that holds them on one CTA: narrow tiles leave more
@@ -789,9 +781,8 @@ size_t plan_tile(TileArgs* a, int sm_count, int forced_workers, void* base) {
   const int workers = a->row_tile == 128 ? sm_count / 2 : sm_count;
   a->num_workers = std::max(1, shared ? workers : workers / a->groups);
   if (forced_workers > 0) a->num_workers = forced_workers;
-  const size_t tasks = shared ? (size_t)a->tiles + (size_t)a->batch * a->groups : (size_t)a->batch;
-  const size_t rows = shared ? (size_t)2 * a->num_workers * a->row_tile + 2 * (size_t)R
-                             : (size_t)2 * a->num_workers * a->groups * a->row_tile;
+  const size_t tasks = shared ? a->tiles : a->batch;
+  const size_t rows = (size_t)2 * a->num_workers * (shared ? 1 : a->groups) * a->row_tile;
   size_t off = 0;
   auto take = [&](size_t bytes) {
     char* p = base ? static_cast<char*>(base) + off : nullptr;
@@ -814,10 +805,11 @@ void tile_schedule(TileArgs* a) {
   // 32 sharing 2,000 44 / 37 / 36 / 38; single, at 0 / 3 / 6 / 9, 16 heads of 128 sequences
   // sharing 1,000 47 / 41 / 41 / 43, 32 heads over a window of 4,096 44 / 42 / 40 / 39).
   a->piece_cost = pc > 0 ? std::min(pc - 1, kMaxPieceCost) : a->row_tile == 128 ? 10 : 3;
-  // Sequences run whole when splitting them would save less than its piece costs: up to 12
-  // pages for a pair (128 heads, whole / split us: 64 windows of 65 pages 75 / 86, of 1 to 34
+  // Sequences (or tiles) run whole when splitting them would save less than it costs: to a
+  // pair, of R rows in all, 10 + R / 512 pages (a piece more per worker, fp32 partials and
+  // their merge; whole / split us: 64 windows of 65 pages for 128 heads 75 / 86, of 1 to 34
   // pages 47 / 53; 16 windows of 66 pages for two queries of 64 heads 59 / 37).
-  const int slack = a->row_tile == 128 ? 12 : 2;
+  const int slack = a->row_tile == 128 ? 10 + a->batch * a->rows / 512 : 2;
   a->whole_slack = knob_value(MLA_KNOB_NUM_WORKERS) > 0 || policy == 1 ? -1 : policy == 2 ? 1 << 30 : slack;
 }
 
@@ -834,9 +826,10 @@ cudaError_t launch_decode_tile(const TileArgs& a, cudaStream_t stream) {
         : a.row_tile == 32 ? launch_tile<32, false>(a, stream)
                            : launch_tile<64, false>(a, stream);
   if (e != cudaSuccess) return e;
-  const int grid = (a.batch * a.rows + kCombineWarps - 1) / kCombineWarps;
-  return shared ? launch_dependent(combine_tile_kernel<true>, grid, kCombineWarps * 32, 0, stream, a)
-                : launch_dependent(combine_tile_kernel<false>, grid, kCombineWarps * 32, 0, stream, a);
+  // As many CTAs as run at once; each takes rows until they are done.
+  const int grid = std::min((a.batch * a.rows + kCombineRows - 1) / kCombineRows, a.sm_count * kCombineCtas);
+  return shared ? launch_dependent(combine_tile_kernel<true>, grid, kCombineThreads, 0, stream, a)
+                : launch_dependent(combine_tile_kernel<false>, grid, kCombineThreads, 0, stream, a);
 }
 
 }  // namespace mla

@@ -29,10 +29,12 @@
 // One buffer each for S and P is enough: while the softmax of step i runs, the tensor cores
 // take the values of step i - 1 and the scores of step i + 1.
 //
-// Roles (416 threads).  Warps 0-7: softmax, 4 threads per row (32 tokens each), and the
-// epilogue.  Warp 8: q' and score loads.  Warp 9: score MMAs (CTA 0).  Warp 10: zeroes value
-// rows that no query sees.  Warp 11: tensor memory, value MMAs (CTA 0).  Warp 12: value loads.
-// (The first warps also write the schedule's records, which the loads should not wait for.)
+// Roles (384 threads; a 13th warp would leave 128 registers a thread, and the spills' traffic
+// shares the path that bounds the products).  Warps 0-7: softmax, 4 threads per row (32 tokens
+// each), and the epilogue.  Warp 8: q' and score loads.  Warp 9: score MMAs (CTA 0).  Warp 10:
+// value loads, and zeroes their rows that no query sees.  Warp 11: tensor memory, value MMAs
+// (CTA 0).  (The first warps also write the schedule's records, which the loads should not
+// wait for.)
 // The lazy running maximum, the roundings and the bounded waits are decode_tile.cu's.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -48,8 +50,8 @@ namespace {
 using namespace sm100;
 
 constexpr int kRows = 128;
-constexpr int kThreads = 416;
-constexpr int kLoadK = 8, kScores = 9, kClean = 10, kValues = 11, kLoadV = 12;  // warps; 0-7 are the softmax's
+constexpr int kThreads = 384;
+constexpr int kLoadK = 8, kScores = 9, kLoadV = 10, kValues = 11;  // warps; 0-7 are the softmax's
 constexpr int kBox = 8192;            // [64 rows x 64 bf16], 128B swizzle
 constexpr int kSlotBytes = 4 * kBox;  // a half page
 constexpr int kKSlots = 3;
@@ -96,40 +98,38 @@ __device__ __forceinline__ uint64_t now_ns() {
   return t;
 }
 
+// What a wait needs besides its barrier, in shared memory: few registers across the kernel.
 struct Ctl {
   int* err;
-  volatile int* abort;
-  uint32_t peer_abort;  // the peer's abort flag (cluster address)
   uint64_t limit_ns;
+  int abort;
+  uint32_t peer_abort;  // the peer's abort flag (cluster address)
 };
 
-__device__ __noinline__ void wait_timed_out(int* err, volatile int* abort, uint32_t peer_abort) {
-  set_device_error(err, MLA_ERR_DEVICE_TIMEOUT);
-  *abort = 1;
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(peer_abort), "r"(1) : "memory");
-}
-
-// Bounded wait on an mbarrier phase; false on timeout or abort.  CTA-scope acquire: what
-// crosses the pair is read by the tensor cores alone.
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const Ctl& c) {
-  if (mbar_try_wait_cta(bar, parity)) return true;
+// Bounded wait on an mbarrier phase; false on timeout (recorded) or abort.  The first try is
+// inlined, the rest is not (it would be at some thirty places).  CTA-scope
+// acquire: what crosses the pair is read by the tensor cores alone.
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, Ctl* c) {
   uint64_t t0 = 0;
+#pragma unroll 1
   for (uint32_t i = 1;; ++i) {
     if (mbar_try_wait_cta(bar, parity)) return true;
     if ((i & 63) == 0) {
-      if (*c.abort) return false;
+      if (*const_cast<volatile int*>(&c->abort)) return false;
       const uint64_t t = now_ns();
       if (t0 == 0) {
         t0 = t;
-      } else if (t - t0 > c.limit_ns) {
-        wait_timed_out(c.err, c.abort, c.peer_abort);
+      } else if (t - t0 > c->limit_ns) {
+        set_device_error(c->err, MLA_ERR_DEVICE_TIMEOUT);
+        *const_cast<volatile int*>(&c->abort) = 1;
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(c->peer_abort), "r"(1) : "memory");
         return false;
       }
     }
   }
 }
-__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, const Ctl& c) {
-  return __all_sync(0xffffffffu, wait_bar(bar, parity, c));
+__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, Ctl* c) {
+  return __all_sync(0xffffffffu, mbar_try_wait_cta(bar, parity) || wait_long(bar, parity, c));
 }
 __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
   const uint64_t t0 = now_ns();
@@ -201,8 +201,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[kNumBars];
   __shared__ uint32_t tmem_base_s;
-  __shared__ int abort_s;
-  __shared__ int bad_s[8];  // [piece % 8] 1 + the last piece that met a page id outside the cache
+  __shared__ Ctl ctl_s;
+  __shared__ uint32_t bad_s[8][4];  // [piece % 8] a bit for each row that a page id outside the cache spoils
   __shared__ RangeScratch range_s;
   __shared__ float mx_s[2][2][2][64];  // [step parity][page][column half][row]
   __shared__ float lsum_s[2][2][64];   // [page][column half][row]
@@ -218,8 +218,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int np = a.block_table ? a.num_pages : a.batch * a.max_blocks;
 
   if (tid == 0) {
-    abort_s = 0;
-    for (int i = 0; i < 8; ++i) bad_s[i] = 0;
+    ctl_s = Ctl{a.err, limit_ns, 0, map_to_rank(smem_u32(&ctl_s.abort), rank ^ 1u)};
+    for (int i = 0; i < 32; ++i) bad_s[i / 4][i % 4] = 0;
     for (int s = 0; s < kKSlots; ++s) {
       mbar_init(bar(kFullK + s), 1);   // CTA 0's producer arms it with both CTAs' bytes
       mbar_init(bar(kEmptyK + s), 1);  // MMA commit
@@ -257,15 +257,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // Everything above overlaps the previous grid on the stream; from here on its writes
   // (the lengths, q', the tables, the cache) are visible.
   grid_dep_wait();
-  derive_range(TaskLengths<kShared>{&a}, kShared ? a.tiles + a.batch * a.groups : a.batch, a.num_workers, a.min_pages,
+  derive_range(TaskLengths<kShared>{&a}, kShared ? a.tiles : a.batch, a.num_workers, a.min_pages,
                a.granule, a.whole_slack, a.piece_cost, a.task, a.err, w, range_s);
   const uint32_t tmem = tmem_base_s;
-  const Ctl ctl{a.err, &abort_s, map_to_rank(smem_u32(&abort_s), rank ^ 1u), limit_ns};
+  Ctl* const ctl = &ctl_s;
   auto bar0 = [&](int i) { return map_to_rank(bar(i), 0); };
 
   if (warp == kLoadK) {
     // ------------------------------------------------------------ q' and score loads
-    PieceLoads<kRows, kShared> ld(a, range_s.rg, grp, np, lane);  // bad pages: the value loads report them
+    PieceLoads<kRows, kShared> ld(a, range_s.rg, grp, np, lane);
     int slot = 0, piece = 0, fills = 0, g = 0;
     uint32_t phase = 1;
     int withheld = -1;
@@ -294,7 +294,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tma_load_3d_pair(sbase + kOffQ, &q_map, 0, qrow, kQTmemBoxes, bar0(kQFull));
       }
       for (int i = 0; i < steps && ok; ++i, ++g) {
-        const int y = ld.row(ld.pc.pa + 2 * i + (int)rank);
+        bool dirty;
+        const int y = ld.row(ld.pc.pa + 2 * i + (int)rank, dirty, nullptr);  // bad pages: the value loads mark the rows
 #pragma unroll 1
         for (int m = 0; m < 2; ++m) {
           // The rope rides on the second half.  That half's slot was last held by the first
@@ -334,19 +335,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int piece = 0, g = 0;
     uint32_t dirty_fills[2] = {0, 0};
     bool ok = true;
+    const uint32_t full0 = bar0(kFullV);
     while (ok && ld.next()) {
       const int steps = (ld.pc.pe - ld.pc.pa + 1) / 2;
+      // The marks four pieces on are those of four pieces back: read, since these loads run
+      // less than three pieces ahead of the softmax.
+      if (lane < 4) bad_s[(piece + 4) & 7][lane] = 0;
+      __syncwarp();
       for (int i = 0; i < steps && ok; ++i, ++g) {
+        bool dirty[2];
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
-          const int p = ld.pc.pa + 2 * i + m;
-          const int y = ld.row(p);
-          const bool dirty = p < ld.pc.pe && page_dirty(ld.k.s, ld.k.s.real(p));
+          const int y = ld.row(ld.pc.pa + 2 * i + m, dirty[m], bad_s[piece & 7]);
           if (!wait_all(bar(kEmptyV + m), (g & 1) ^ 1, ctl)) { ok = false; break; }
           if (lane == 0) {
-            if (ld.bad) *const_cast<volatile int*>(&bad_s[piece & 7]) = piece + 1;
             const uint32_t dst = sbase + kOffV + m * kSlotBytes;
-            if (dirty) {
+            if (dirty[m]) {
               mbar_expect_tx(bar(kDirty + m), kSlotBytes);
               tma_load_3d(dst, &kv_map, 0, y, 4 * (int)rank, bar(kDirty + m));
             } else {
@@ -357,7 +361,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               tma_load_3d_pair(dst, &kv_map, 0, y, 4 * (int)rank, bar0(kFullV + m));
             }
           }
-          dirty_fills[m] += dirty ? 1u : 0u;
+          dirty_fills[m] += dirty[m] ? 1u : 0u;
+        }
+        if (!ok) break;
+        // Rows [h0, h1) and [e0, 64) of a dirty page are cleared here: the next step's loads
+        // wait for this one's slots anyway.
+#pragma unroll 1
+        for (int m = 0; m < 2; ++m) {
+          if (!(m ? dirty[1] : dirty[0])) continue;
+          int t0, e0;
+          ld.page(ld.pc.pa + 2 * i + m, t0, e0);
+          const int h0 = kShared ? 0 : max(ld.k.s.hole0 - t0, 0), h1 = kShared ? 0 : max(h0, min(ld.k.s.hole1 - t0, kPage));
+          const int nrow = (h1 - h0) + (kPage - e0);
+          if (!wait_all(bar(kDirty + m), ((m ? dirty_fills[1] : dirty_fills[0]) - 1) & 1, ctl)) { ok = false; break; }
+          uint8_t* st = smem + kOffV + m * kSlotBytes;
+#pragma unroll 1
+          for (int idx = lane; idx < nrow * 8; idx += 32) {
+            const int r = idx / 8, row = r < h1 - h0 ? h0 + r : e0 + (r - (h1 - h0));
+#pragma unroll
+            for (int box = 0; box < 4; ++box)
+              *reinterpret_cast<uint4*>(st + box * kBox + row * 128 + (idx % 8) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) arrive_cta0(rank, bar(kFullV + m), full0 + 8 * m);
         }
         if (i == 0) ld.look();
       }
@@ -462,36 +489,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       drain_wait(bar(kDrain + 1), 0, limit_ns);
     }
     __syncwarp();
-  } else if (warp == kClean) {
-    // ------------------------------------------------------------ value rows in no query's sight
-    PieceIter<kShared> pi(range_s.rg);
-    Piece pc;
-    uint32_t dpar = 0;
-    bool ok = true;
-    const uint32_t full0 = bar0(kFullV);
-    while (ok && pi.next(pc, a)) {
-      const Task k = load_task<kRows, kShared>(a, pc.t, grp);
-      for (int p = pc.pa; p < pc.pe && ok; ++p) {
-        const int real = k.s.real(p), t0 = real * kPage, m = (p - pc.pa) & 1;
-        if (!page_dirty(k.s, real)) continue;
-        if (!wait_all(bar(kDirty + m), (dpar >> m) & 1u, ctl)) { ok = false; break; }
-        dpar ^= 1u << m;
-        // Rows [h0, h1) and [e0, 64) of the page.
-        const int h0 = max(k.s.hole0 - t0, 0), h1 = max(h0, min(k.s.hole1 - t0, kPage));
-        const int e0 = min(max(k.s.T - t0, 0), kPage);
-        const int nrow = (h1 - h0) + (kPage - e0);
-        uint8_t* st = smem + kOffV + m * kSlotBytes;
-        for (int idx = lane; idx < nrow * 8; idx += 32) {
-          const int r = idx / 8, row = r < h1 - h0 ? h0 + r : e0 + (r - (h1 - h0));
-#pragma unroll
-          for (int box = 0; box < 4; ++box)
-            *reinterpret_cast<uint4*>(st + box * kBox + row * 128 + (idx % 8) * 16) = make_uint4(0, 0, 0, 0);
-        }
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) arrive_cta0(rank, bar(kFullV + m), full0 + 8 * m);
-      }
-    }
   } else {
     // ------------------------------------------------------------ softmax and epilogue
     const int q = warp & 3;                     // TMEM lane quadrant
@@ -545,23 +542,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     };
     PieceIter<kShared> pi(range_s.rg), pn(range_s.rg);  // pn runs one piece ahead
     Piece pc, nc;
-    // A piece's task and what this row sees of it: tokens t < end with t < sinks or t >= from
-    // (a row past the tile's sees none).  Looked up a piece ahead, under the epilogue.
+    // A piece's task and what this row sees of it, looked up a piece ahead, under the epilogue.
     struct RowTask {
       Task t;
-      int end, from;
+      RowSight sight;
     };
     auto row_task = [&](const Piece& x) {
-      RowTask r{load_task<kRows, kShared>(a, x.t, grp), -1, 0};
-      if (row < r.t.live) {
-        if (kShared && x.t < a.tiles) {
-          const int n = r.t.row0 + row, b = n / a.rows;
-          r.end = min(r.t.s.T, r.t.s.T + a.seqlens[b] - a.s_q + 1 + (n - b * a.rows) / a.heads);
-        } else {
-          r.end = r.t.s.T - a.s_q + 1 + (r.t.srow + row) / a.heads;
-          if (!kShared) r.from = r.end - a.window;
-        }
-      }
+      RowTask r{load_task<kRows, kShared>(a, x.t, grp), {}};
+      r.sight = row_sight<kShared>(a, r.t, row);
       return r;
     };
     bool have_next = pn.next(nc, a);
@@ -572,11 +560,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     while (ok && pi.next(pc, a)) {
       have_next = pn.next(nc, a);
       const RowTask k = kn;
-      const int steps = (pc.pe - pc.pa + 1) / 2, end = k.end, from = k.from;
+      const int steps = (pc.pe - pc.pa + 1) / 2;
+      PageRef ref{};  // lane l: list page pa + 32 (i / 16) + l
       float m = -INFINITY, l = 0.f;
       for (int i = 0; i < steps && ok; ++i) {
         const int gs = g + i, u = gs & 1;
         const int p = pc.pa + 2 * i + hh;
+        if ((i & 15) == 0) ref = page_ref<kShared>(a, k.t, min(pc.pa + 2 * i + lane, pc.pe - 1));
         if (!wait_all(bar(kSFull), gs & 1, ctl)) { ok = false; break; }
         tc_fence_after();
         float y[32];
@@ -590,9 +580,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) arrive_cta0(rank, bar(kSFree), sfree0);
-        const int t0 = k.t.s.real(p) * kPage + 32 * c;
-        uint32_t see = p < pc.pe ? below(end - t0) : 0u;
-        if (!kShared) see &= below(a.sinks - t0) | ~below(from - t0);
+        const int t0 = __shfl_sync(0xffffffffu, ref.page, 2 * (i & 15) + hh) * kPage + 32 * c;
+        uint32_t see = 0;
+        if constexpr (kShared) {
+          const int seq = __shfl_sync(0xffffffffu, ref.seq, 2 * (i & 15) + hh);
+          if (p < pc.pe) see = seq < 0 ? below(k.sight.prefix_end - t0) : seq == k.sight.seq ? below(k.sight.end - t0) : 0u;
+        } else if (p < pc.pe) {
+          see = below(k.sight.end - t0) & (below(a.sinks - t0) | ~below(k.sight.from - t0));
+        }
         const uint64_t s2 = f2_pack(scale2, scale2);
 #pragma unroll
         for (int j = 0; j < 32; j += 2) f2_unpack(f2_mul(f2_pack(y[j], y[j + 1]), s2), y[j], y[j + 1]);
@@ -675,7 +670,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const float l_row = (lsum_s[0][0][h] + lsum_s[0][1][h]) + (lsum_s[1][0][h] + lsum_s[1][1][h]);
       if (!wait_all(bar(kODone), ge & 1, ctl)) { ok = false; break; }
       tc_fence_after();
-      const bool bad = *const_cast<volatile int*>(&bad_s[piece & 7]) == piece + 1;
+      const bool bad = k.sight.bad || ((const_cast<volatile uint32_t&>(bad_s[piece & 7][row >> 5]) >> (row & 31)) & 1u);
       const bool none = l_row == 0.f;  // the row sees no token of the piece
       const float inv = bad ? NAN : (none ? 0.f : 1.f / l_row);
       const PieceOut to = piece_out<kRows, kShared>(a, k.t, pc, pi.rg, w, grp);
@@ -701,7 +696,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (tid == 0) grid_dep_launch_dependents();  // the combine grid may launch (it waits for this grid's writes)
   tc_fence_before();
   __syncthreads();
-  if (abort_s) {
+  if (ctl_s.abort) {
     // A load whose barrier the peer never armed has no phase to wait for: give it time to land.
     const uint64_t t0 = now_ns();
     while (now_ns() - t0 < 100000) {

@@ -105,11 +105,11 @@ cudaError_t launch_decode(int kernel, const DecodeArgs& a, cudaStream_t stream);
 int decode_granule(int kernel);
 
 // Sliding-window and shared-prefix decode: query rows in tiles of row_tile (16, 32 or 64
-// with one CTA per worker, decode_tile.cu, or 128 with a CTA pair, decode_tile_pair.cu).  The schedule's entries ("tasks") are, for a
-// window, the sequences (worker w of group g walks the pages for rows [g row_tile, +) of
-// each sequence, so the `groups` CTAs or pairs of one worker read the same pages side by side);
-// for a shared prefix, first the prefix once for each of the `tiles` row tiles of the
-// whole batch, then each sequence's own tokens once for each of its groups.
+// with one CTA per worker, decode_tile.cu, or 128 with a CTA pair, decode_tile_pair.cu).  The schedule's entries ("tasks") are,
+// for a window, the sequences (worker w of group g walks the pages for rows [g row_tile, +)
+// of each sequence, so the `groups` CTAs or pairs of one worker read the same pages side by
+// side); for a shared prefix, the `tiles` row tiles of the whole batch, each with the
+// prefix's pages and then the own pages of the sequences that have rows in it.
 struct TileArgs {
   const __nv_bfloat16* q;
   const __nv_bfloat16* kv;
@@ -125,13 +125,11 @@ struct TileArgs {
   float scale;
   int* err;
   int row_tile, groups, tiles;
-  // Workspace: a record per task; split partials [2 workers][groups (window) or 1][row_tile]
-  // and, for a shared prefix, the unsplit results of all rows against the prefix and
-  // against their own tokens.
+  // Workspace: a record per task; split partials [2 workers][groups (window) or 1][row_tile].
   SeqInfo* task;
   float* part_lse;
   float* part_o;
-  int num_workers;
+  int num_workers, sm_count;
   int min_pages, granule, whole_slack, piece_cost;
   int wait_limit, withhold_arrive;
 };

@@ -22,8 +22,11 @@ __device__ __forceinline__ void warm_params(const TileArgs& a, int tid) {
 }
 
 // ---------------------------------------------------------------- tasks
-// The pages of a task: page p of its list is page real(p) of its table; the first `ns`
-// hold the sinks, the rest run from the window's first page to the last.
+// Window: a task is a sequence; page p of its list is page real(p) of its table; the first
+// `ns` hold the sinks, the rest run from the window's first page to the last.
+// Shared prefix: a task is a tile of query rows of the whole batch; its list holds the
+// prefix's pages, then the own pages of each sequence that has rows in the tile (a page of
+// one sequence is hidden from the others' rows).
 struct Span {
   int T, n, ns, skip;
   int hole0, hole1;  // tokens [hole0, hole1) are in no query's sight (between sinks and window)
@@ -43,77 +46,166 @@ __device__ __forceinline__ Span window_span(const TileArgs& a, int T) {
   return s;
 }
 
+__device__ __forceinline__ bool bad_length(int T, int blocks) { return T < 0 || T > blocks * kPage; }
+__device__ __forceinline__ int own_pages(const TileArgs& a, int b) { return seq_pages(a.seqlens, a.max_blocks, b); }
+__device__ __forceinline__ int prefix_pages(const TileArgs& a) { return seq_pages(a.prefix_len, a.prefix_blocks, 0); }
+// The first and last sequence with rows in a tile of the batch.
+__device__ __forceinline__ int tile_seq0(const TileArgs& a, int t) { return t * a.row_tile / a.rows; }
+__device__ __forceinline__ int tile_seq1(const TileArgs& a, int t) { return (min((t + 1) * a.row_tile, a.batch * a.rows) - 1) / a.rows; }
+
 template <bool kShared>
 struct TaskLengths {
   const TileArgs* a;
-  __device__ __forceinline__ int raw(int t) const {
-    if (!kShared) return a->seqlens[t];
-    return t < a->tiles ? *a->prefix_len : a->seqlens[(t - a->tiles) / a->groups];
-  }
-  __device__ __forceinline__ int cap(int t) const { return kShared && t < a->tiles ? a->prefix_blocks : a->max_blocks; }
   __device__ __forceinline__ bool bad(int t) const {
-    const int T = raw(t);
-    return T < 0 || T > cap(t) * kPage;
+    return kShared ? bad_length(*a->prefix_len, a->prefix_blocks) : bad_length(a->seqlens[t], a->max_blocks);
   }
   __device__ __forceinline__ int pages(int t) const {
-    const int T = raw(t);
-    if (!kShared) return window_span(*a, T).n;
-    return (T < 0 || T > cap(t) * kPage) ? 0 : (T + kPage - 1) / kPage;
+    if constexpr (!kShared) return window_span(*a, a->seqlens[t]).n;
+    if (bad(t)) return 0;
+    int n = prefix_pages(*a);
+    const int b1 = tile_seq1(*a, t);
+#pragma unroll 8
+    for (int b = tile_seq0(*a, t); b <= b1; ++b) n += own_pages(*a, b);
+    return n;
   }
 };
 
+// Pages of a task, taken by a whole warp together.  (Not inlined, like page_ref_shared: twelve
+// warps run six roles, and seldom-run code in their loops costs instruction cache.)
+static __device__ __noinline__ int tile_pages(const TileArgs& a, int t) {
+  if (bad_length(*a.prefix_len, a.prefix_blocks)) return 0;
+  int n = 0;
+  const int b1 = tile_seq1(a, t);
+#pragma unroll 1
+  for (int b = tile_seq0(a, t) + (threadIdx.x & 31); b <= b1; b += 32) n += own_pages(a, b);
+  return prefix_pages(a) + __reduce_add_sync(0xffffffffu, n);
+}
+template <bool kShared>
+__device__ __forceinline__ int task_pages(const TileArgs& a, int t) {
+  if constexpr (kShared) return tile_pages(a, t);
+  else return window_span(a, a.seqlens[t]).n;
+}
+
 struct Task {
-  Span s;
-  const int32_t* table;  // null: page = base + real
-  int base;
+  Span s;          // window: the sequence's; shared: the prefix's (T and n alone)
+  int b0, b1;      // the sequence; shared: the first and last with rows in the tile
   int row0, live;  // first query row of the whole batch's, rows of the tile
-  int srow;        // row0 within its sequence (window, own tokens)
+  int srow;        // window: row0 within its sequence
 };
 
 template <int N, bool kShared>
 __device__ __forceinline__ Task load_task(const TileArgs& a, int t, int g) {
   Task k;
-  k.base = 0;
-  if (kShared && t < a.tiles) {
-    const int T = *a.prefix_len;
-    k.s = Span{T, (T + kPage - 1) / kPage, (T + kPage - 1) / kPage, 0, 0, 0};
-    k.table = a.prefix_table;
+  if constexpr (kShared) {
+    k.s = Span{*a.prefix_len, prefix_pages(a), 0, 0, 0, 0};
+    k.b0 = tile_seq0(a, t);
+    k.b1 = tile_seq1(a, t);
     k.row0 = t * N;
     k.live = min(N, a.batch * a.rows - k.row0);
     k.srow = 0;
-    return k;
+  } else {
+    k.s = window_span(a, a.seqlens[t]);
+    k.b0 = k.b1 = t;
+    k.srow = g * N;
+    k.row0 = t * a.rows + k.srow;
+    k.live = min(N, a.rows - k.srow);
   }
-  const int b = kShared ? (t - a.tiles) / a.groups : t;
-  if (kShared) g = (t - a.tiles) % a.groups;
-  const int T = a.seqlens[b];
-  k.s = kShared ? Span{T, (T + kPage - 1) / kPage, (T + kPage - 1) / kPage, 0, 0, 0} : window_span(a, T);
-  k.table = a.block_table ? a.block_table + (size_t)b * a.max_blocks : nullptr;
-  k.base = b * a.max_blocks;
-  k.srow = g * N;
-  k.row0 = b * a.rows + k.srow;
-  k.live = min(N, a.rows - k.srow);
   return k;
+}
+
+// A page of a task's list: its sequence (-1: the prefix), its index in that table, and the
+// tokens of the sequence (or prefix).
+struct PageRef {
+  int seq, page, T;
+  __device__ __forceinline__ int valid_rows() const { return min(max(T - page * kPage, 0), kPage); }
+};
+
+// Page q of the own pages of sequences b0..b1 for every lane of a warp (each its own q; q < 0:
+// page q + prefix of the prefix, whose length is T).
+static __device__ __noinline__ PageRef page_ref_shared(const TileArgs& a, int q, int prefix, int T0, int b0, int b1) {
+  const int lane = threadIdx.x & 31;
+  PageRef r{-1, q + prefix, T0};
+  bool open = q >= 0;
+  // 32 sequences at a time: the ends of their pages in the list, and each lane's search.
+#pragma unroll 1
+  for (; b0 <= b1 && __any_sync(0xffffffffu, open); b0 += 32) {
+    const int b = b0 + lane;
+    const int T = b <= b1 ? a.seqlens[b] : 0;
+    const int n = bad_length(T, a.max_blocks) ? 0 : (T + kPage - 1) / kPage;
+    int end = n;
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, end, o);
+      if (lane >= o) end += y;
+    }
+    const int total = __shfl_sync(0xffffffffu, end, 31);
+    int j = 0;  // the first sequence whose end is above q
+#pragma unroll 1
+    for (int o = 16; o; o >>= 1)
+      if (__shfl_sync(0xffffffffu, end, j + o - 1) <= q) j += o;
+    const int first = __shfl_sync(0xffffffffu, end - n, j), Tj = __shfl_sync(0xffffffffu, T, j);
+    if (open && q < total) {
+      r = PageRef{b0 + j, q - first, Tj};
+      open = false;
+    }
+    q -= total;
+  }
+  return r;
+}
+// Page p of a task's list for every lane of a warp (each its own p, inside the list).
+template <bool kShared>
+__device__ __forceinline__ PageRef page_ref(const TileArgs& a, const Task& k, int p) {
+  if constexpr (kShared) return page_ref_shared(a, p - k.s.n, k.s.n, k.s.T, k.b0, k.b1);
+  else return {k.b0, k.s.real(p), k.s.T};
+}
+
+// What row `row` of a task's tile sees: tokens t < end of its sequence's own (window: all)
+// tokens with t < sinks or t >= from; of a shared prefix the tokens t < prefix_end.  `seq` is
+// the row's sequence, and `bad` says that its length is invalid.
+struct RowSight {
+  int seq, end, from, prefix_end;
+  bool bad;
+};
+
+template <bool kShared>
+__device__ __forceinline__ RowSight row_sight(const TileArgs& a, const Task& k, int row) {
+  RowSight r{-2, -1, 0, -1, false};  // a row past the tile's sees nothing
+  if (row >= k.live) return r;
+  if constexpr (kShared) {
+    const int n = k.row0 + row;
+    r.seq = n / a.rows;
+    const int T = a.seqlens[r.seq];
+    r.bad = bad_length(T, a.max_blocks);
+    r.end = T - a.s_q + 1 + (n - r.seq * a.rows) / a.heads;
+    r.prefix_end = min(k.s.T, k.s.T + r.end);
+  } else {
+    r.seq = k.b0;
+    r.end = k.s.T - a.s_q + 1 + (k.srow + row) / a.heads;
+    r.from = r.end - a.window;
+  }
+  return r;
 }
 
 struct Piece {
   int t, pa, pe;
+  int n;  // pages of the whole task
 };
 
-// Iterates the pieces of a worker's range in schedule order.
+// Iterates the pieces of a worker's range in schedule order (by a whole warp).
 template <bool kShared>
 struct PieceIter {
   WorkerRange rg;
   int t;
   __device__ explicit PieceIter(const volatile WorkerRange& r) : rg{r.b0, r.p0, r.b1, r.p1}, t(r.b0) {}
-  __device__ bool next(Piece& pc, const TileArgs& a) {
+  __device__ __forceinline__ bool next(Piece& pc, const TileArgs& a) {
     if (rg.b0 < 0) return false;
-    const TaskLengths<kShared> len{&a};
+#pragma unroll 1
     while (t <= rg.b1) {
-      const int cur = t++;
+      const int cur = t++, n = task_pages<kShared>(a, cur);
       const int pa = cur == rg.b0 ? rg.p0 : 0;
-      const int pe = cur == rg.b1 ? rg.p1 : len.pages(cur);
+      const int pe = cur == rg.b1 ? rg.p1 : n;
       if (pa < pe) {
-        pc = {cur, pa, pe};
+        pc = {cur, pa, pe, n};
         return true;
       }
     }
@@ -131,77 +223,101 @@ struct PieceOut {
 template <int N, bool kShared>
 __device__ __forceinline__ PieceOut piece_out(const TileArgs& a, const Task& k, const Piece& pc, const WorkerRange& rg, int w,
                                               int grp) {
-  if (pc.pa == 0 && pc.pe == k.s.n) {
-    if (!kShared) return {true, (size_t)k.row0};
-    return {false, (size_t)2 * a.num_workers * N + (pc.t < a.tiles ? 0 : a.batch * a.rows) + k.row0};
-  }
+  if (pc.pa == 0 && pc.pe == pc.n) return {true, (size_t)k.row0};
   const size_t slot = pc.t == rg.b0 ? w : a.num_workers + w;
   return {false, (kShared ? slot : slot * a.groups + grp) * N};
 }
 
-// A loading warp's walk over its worker's pages.  The next piece's task and first page ids
-// are read (look) while the current piece loads, so that a piece starts without waiting for
-// its table.
+// Whether some row of a page is in no query's sight.
+template <bool kShared>
+__device__ __forceinline__ bool page_dirty(const Task& k, const PageRef& r) {
+  const int t0 = r.page * kPage;
+  return r.T < t0 + kPage || (!kShared && max(k.s.hole0, t0) < min(k.s.hole1, t0 + kPage));
+}
+
+// Sets bits [r0, r1) of `words` words.
+static __device__ __noinline__ void mark_rows(uint32_t* bits, int words, int r0, int r1) {
+#pragma unroll 1
+  for (int i = 0; i < words; ++i) {
+    const int lo = max(r0 - 32 * i, 0), hi = min(r1 - 32 * i, 32);
+    if (lo < hi) atomicOr(bits + i, (hi == 32 ? 0xffffffffu : (1u << hi) - 1u) & ~((1u << lo) - 1u));
+  }
+}
+
+// A loading warp's walk over its worker's pages, 32 of the list at a time.  The next piece's
+// task and first pages are looked up while the current piece loads, so that a piece starts
+// without waiting for its table.
 template <int N, bool kShared>
 struct PieceLoads {
+  static constexpr int kWords = (N + 31) / 32;
   const TileArgs& a;
   const int grp, np, lane;
   PieceIter<kShared> it;
   Piece pc, nc;
   Task k, nk;
-  int ids, nids, at;  // lane l holds the id of list page at + l
-  bool have, fresh, bad;
+  int id, nid, at;     // lane l holds the page id of list page at + l,
+  PageRef ref, nref;   // and where it stands
+  bool have, fresh;
 
   __device__ PieceLoads(const TileArgs& args, const volatile WorkerRange& rg, int g, int num_pages, int l)
       : a(args), grp(g), np(num_pages), lane(l), it(rg) {
     look();
   }
-  __device__ __forceinline__ int id(const Task& t, const Piece& p, int pp) const {
-    return pp < p.pe ? (t.table ? t.table[t.s.real(pp)] : t.base + t.s.real(pp)) : 0;
+  __device__ __forceinline__ void read(const Task& t, const Piece& p, int p0, int& id_, PageRef& r) const {
+    r = page_ref<kShared>(a, t, min(p0 + lane, p.pe - 1));
+    if (kShared && r.seq < 0) id_ = a.prefix_table[r.page];
+    else id_ = a.block_table ? a.block_table[(size_t)r.seq * a.max_blocks + r.page] : r.seq * a.max_blocks + r.page;
   }
   __device__ __forceinline__ void look() {
     have = it.next(nc, a);
     if (!have) return;
     nk = load_task<N, kShared>(a, nc.t, grp);
-    nids = id(nk, nc, nc.pa + lane);
+    read(nk, nc, nc.pa, nid, nref);
   }
   // The piece looked up last becomes the current one.
   __device__ __forceinline__ bool next() {
     if (!have) return false;
     pc = nc;
     k = nk;
-    ids = nids;
+    id = nid;
+    ref = nref;
     at = pc.pa;
     fresh = true;
-    bad = have = false;
+    have = false;
     return true;
   }
-  // First row of list page p; a page id outside the cache gives the row that reads zeros,
-  // the error, and `bad` for the rest of the piece.
-  __device__ __forceinline__ int row(int p) {
+  // First row of list page p and whether the page is dirty; pages past the piece and page
+  // ids outside the cache give the row that reads zeros, the latter also the error and, in
+  // `bad` (a bit per row of the tile), the rows that see the page.
+  __device__ __forceinline__ int row(int p, bool& dirty, uint32_t* bad) {
+    dirty = false;
     if (p >= pc.pe) return np * kPage;
     if (p >= at + 32) {
       at = p;
-      ids = id(k, pc, p + lane);
+      read(k, pc, p, id, ref);
       fresh = true;
     }
     if (fresh) {
       fresh = false;
-      if (__any_sync(0xffffffffu, (unsigned)ids >= (unsigned)np)) {
-        if ((unsigned)ids >= (unsigned)np) set_device_error(a.err, MLA_ERR_DEVICE_BAD_PAGE);
-        bad = true;
+      if ((unsigned)id >= (unsigned)np) {
+        set_device_error(a.err, MLA_ERR_DEVICE_BAD_PAGE);
+        if (bad) {
+          const bool all = !kShared || ref.seq < 0;
+          mark_rows(bad, kWords, all ? 0 : max(ref.seq * a.rows - k.row0, 0), all ? N : min((ref.seq + 1) * a.rows - k.row0, N));
+        }
       }
+      __syncwarp();
     }
-    const int v = __shfl_sync(0xffffffffu, ids, p - at);
+    dirty = __shfl_sync(0xffffffffu, (int)page_dirty<kShared>(k, ref), p - at) != 0;
+    const int v = __shfl_sync(0xffffffffu, id, p - at);
     return (unsigned)v < (unsigned)np ? v * kPage : np * kPage;
   }
+  // The first token and the valid rows of list page p, whose row() was just asked for.
+  __device__ __forceinline__ void page(int p, int& t0, int& rows) const {
+    t0 = __shfl_sync(0xffffffffu, ref.page, p - at) * kPage;
+    rows = __shfl_sync(0xffffffffu, ref.valid_rows(), p - at);
+  }
 };
-
-// Whether some row of table page `real` is in no query's sight.
-__device__ __forceinline__ bool page_dirty(const Span& s, int real) {
-  const int t0 = real * kPage;
-  return s.T < t0 + kPage || (max(s.hole0, t0) < min(s.hole1, t0 + kPage));
-}
 
 // Bits [0, x) of a word.
 __device__ __forceinline__ uint32_t below(int x) { return x <= 0 ? 0u : x >= 32 ? 0xffffffffu : (1u << x) - 1u; }
