@@ -92,10 +92,10 @@ def _check(status: int) -> None:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream) -> int:
+def _stream(stream, dev: int | None = None) -> int:
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(torch.cuda.current_device() if dev is None else dev)
         return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -217,7 +217,7 @@ def mla_absorb_o(out_latent, w_uv, out, stream=None) -> None:
         dev = torch.cuda.current_device()
         _check(lib.mla_absorb_o_bf16(_here(out_latent, "out_latent", torch.bfloat16, (B, H, D_LATENT), dev),
                                      _here(w_uv, "w_uv", torch.bfloat16, (H, D_LATENT, D_V), dev),
-                                     _here(out, "out", torch.float32, (B, H, D_V), dev), B, H, _stream(stream)))
+                                     _here(out, "out", torch.float32, (B, H, D_V), dev), B, H, _stream(stream, dev)))
         return
     _need(out_latent, "out_latent", torch.float32, (B, H, D_LATENT))
     _need(w_uv, "w_uv", torch.bfloat16, (H, D_LATENT, D_V))
@@ -296,7 +296,7 @@ def mla_append(c_kv, k_rope, kv_cache, block_table, cache_seqlens, cos_sin, cu_t
         p_o, s_o = _rows_view(q_out, "q_out", (N, H, D_ROPE), dev)
     kv, max_blocks, num_pages, bt = _cache_here(kv_cache, block_table, B, dev)
     _check(lib.mla_append(p_c, p_k, p_q, p_o, table, cu, lens, off, bt, kv, s_c[0], s_k[0], s_q[0], s_q[1], s_o[0], s_o[1], N,
-                          B, H, num_pages, max_blocks, cos_sin.shape[0], 1 if interleaved else 0, _stream(stream)))
+                          B, H, num_pages, max_blocks, cos_sin.shape[0], 1 if interleaved else 0, _stream(stream, dev)))
 
 
 def _query_shape(q):
@@ -338,7 +338,7 @@ def mla_decode_window(q, kv_cache, block_table, cache_seqlens, out, lse, softmax
     kv, max_blocks, num_pages, bt = _cache_here(kv_cache, block_table, B, dev)
     ws = _workspace(workspace, lib.mla_decode_window_workspace_size(B, SQ, H), stream, q.device, dev)
     _check(lib.mla_decode_window(p_q, kv, bt, lens, p_o, p_l, B, SQ, H, num_pages, max_blocks, window, sinks, softmax_scale,
-                                 ws.data_ptr(), ws.numel(), _stream(stream)))
+                                 ws.data_ptr(), ws.numel(), _stream(stream, dev)))
 
 
 def mla_decode_window_workspace_size(batch: int, s_q: int, heads: int) -> int:
@@ -366,7 +366,7 @@ def mla_decode_shared(q, kv_cache, prefix_table, prefix_len, block_table, cache_
     kv, max_blocks, num_pages, bt = _cache_here(kv_cache, block_table, B, dev)
     ws = _workspace(workspace, lib.mla_decode_shared_workspace_size(B, SQ, H), stream, q.device, dev)
     _check(lib.mla_decode_shared(p_q, kv, ptab, plen, bt, lens, p_o, p_l, B, SQ, H, num_pages, prefix_table.shape[0],
-                                 max_blocks, softmax_scale, ws.data_ptr(), ws.numel(), _stream(stream)))
+                                 max_blocks, softmax_scale, ws.data_ptr(), ws.numel(), _stream(stream, dev)))
 
 
 def mla_decode_shared_workspace_size(batch: int, s_q: int, heads: int) -> int:

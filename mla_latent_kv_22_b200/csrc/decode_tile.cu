@@ -206,6 +206,21 @@ __device__ __forceinline__ void store_o(uint32_t taddr, const float* inv, int li
   }
 }
 
+// Zeroes the values that are not finite of a page's tokens (bit j of lanes 0-15's word is token j, of lanes
+// 16-31's token 32 + j) in the four boxes of either half.  By a whole warp, between the page's
+// scores and its second product.
+__device__ __noinline__ void drop_values(uint8_t* h0, uint8_t* h1, uint32_t word, int lane) {
+#pragma unroll 1
+  for (int t = 0; t < 64; ++t) {
+    if (!((__shfl_sync(0xffffffffu, word, t >> 1 & 16) >> (t & 31)) & 1u)) continue;
+    const int at = (lane >> 3) * kBox + t * 128 + (lane & 7) * 16;  // 32 chunks of 16 bytes
+    *reinterpret_cast<uint4*>(h0 + at) = finite_chunk(*reinterpret_cast<uint4*>(h0 + at));
+    *reinterpret_cast<uint4*>(h1 + at) = finite_chunk(*reinterpret_cast<uint4*>(h1 + at));
+  }
+  fence_proxy_async();
+  __syncwarp();
+}
+
 template <int N, bool kShared>
 __global__ void __launch_bounds__(kThreads, 1)
     decode_tile_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap rope_map,
@@ -503,6 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++meets;
       return r;
     };
+    const bool mixed = mixed_pages<kShared>(a);
     uint8_t* const prow = smem + Lay::kOffP + (row < N ? row : 0) * 128;
     constexpr int kOBufs = Lay::kOBufs;
     PieceIter<kShared> pi(range_s.rg);
@@ -535,16 +551,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(bar(kSFree + u));
         if (holds) {
           const int t0 = __shfl_sync(0xffffffffu, ref.page, i & 31) * kPage + 32 * half;
+          const int seq = kShared ? __shfl_sync(0xffffffffu, ref.seq, i & 31) : 0;
           uint32_t see;
-          if constexpr (kShared) {
-            const int seq = __shfl_sync(0xffffffffu, ref.seq, i & 31);
+          if constexpr (kShared)
             see = seq < 0 ? below(sight.prefix_end - t0) : seq == sight.seq ? below(sight.end - t0) : 0u;
-          } else {
+          else
             see = below(sight.end - t0) & (below(a.sinks - t0) | ~below(sight.from - t0));
-          }
           const uint64_t s2 = f2_pack(scale2, scale2);
 #pragma unroll
           for (int j = 0; j < 32; j += 2) f2_unpack(f2_mul(f2_pack(y[j], y[j + 1]), s2), y[j], y[j + 1]);
+          if (mixed && (a.s_q > 1 || seq >= 0)) {
+            // The page's values are here (its scores are), and the second product waits for P.
+            const uint32_t d = nonfinite_seen(y, see);
+            const uint32_t d0 = __reduce_or_sync(0xffffffffu, half ? 0u : d), d1 = __reduce_or_sync(0xffffffffu, half ? d : 0u);
+            if (d0 | d1) {
+              uint8_t* const ring = smem + Lay::kOffRing;
+              drop_values(ring + 2 * gs % kSlots * kSlotBytes, ring + (2 * gs + 1) % kSlots * kSlotBytes, half ? d1 : d0, lane);
+            }
+          }
           if (!__all_sync(0xffffffffu, see == 0xffffffffu)) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) y[j] = ((see >> j) & 1u) ? y[j] : -INFINITY;

@@ -193,7 +193,31 @@ __device__ __forceinline__ void store_rows(uint32_t taddr, float inv, uint8_t* b
   }
 }
 
-template <bool kShared>
+// Zeroes the values that are not finite of a step's tokens, in both CTAs: bit j of lane w's
+// word is token 32 w + j, in the four boxes of slot w / 2.  By a whole warp of CTA 0, with the
+// values landed.
+__device__ __noinline__ void drop_values(uint32_t v, uint32_t word, int lane) {
+#pragma unroll 1
+  for (int t = 0; t < 128; ++t) {
+    if (!((__shfl_sync(0xffffffffu, word, t >> 5) >> (t & 31)) & 1u)) continue;
+    // Four boxes of 128 bytes: 32 chunks of 16, one per lane and CTA.
+    const uint32_t at = v + (t >> 6) * kSlotBytes + (lane >> 3) * kBox + (t & 63) * 128 + (lane & 7) * 16;
+#pragma unroll 1
+    for (int r = 0; r < 2; ++r) {
+      const uint32_t ca = map_to_rank(at, r);
+      uint4 x;
+      asm volatile("ld.shared::cluster.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(ca) : "memory");
+      x = finite_chunk(x);
+      asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(ca), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
+    }
+  }
+  asm volatile("fence.proxy.async;" ::: "memory");
+  asm volatile("fence.acq_rel.cluster;" ::: "memory");
+  __syncwarp();
+}
+
+// kMixed: mixed_pages(a).   A copy of its own: the check costs up to 6% where it is not needed.
+template <bool kShared, bool kMixed>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     decode_tile_pair_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap rope_map,
                             const __grid_constant__ CUtensorMap q_map, const __grid_constant__ TileArgs a,
@@ -204,6 +228,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __shared__ Ctl ctl_s;
   __shared__ uint32_t bad_s[8][4];  // [piece % 8] a bit for each row that a page id outside the cache spoils
   __shared__ RangeScratch range_s;
+  __shared__ uint32_t drop_s[4][4];  // CTA 0: [step % 4][32 tokens] to be looked at (nonfinite_seen)
   __shared__ float mx_s[2][2][2][64];  // [step parity][page][column half][row]
   __shared__ float lsum_s[2][2][64];   // [page][column half][row]
 
@@ -220,6 +245,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     ctl_s = Ctl{a.err, limit_ns, 0, map_to_rank(smem_u32(&ctl_s.abort), rank ^ 1u)};
     for (int i = 0; i < 32; ++i) bad_s[i / 4][i % 4] = 0;
+    for (int i = 0; i < 16; ++i) drop_s[i / 4][i % 4] = 0;
     for (int s = 0; s < kKSlots; ++s) {
       mbar_init(bar(kFullK + s), 1);   // CTA 0's producer arms it with both CTAs' bytes
       mbar_init(bar(kEmptyK + s), 1);  // MMA commit
@@ -461,7 +487,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       Piece pc;
       constexpr uint64_t kKMajor = desc_sw128_const(16, 1024), kMNMajor = desc_sw128_const(kBox, 1024);
       const uint64_t dp = kKMajor | desc_addr(sbase + kOffP), dv = kMNMajor | desc_addr(sbase + kOffV);
-      int piece = 0, g = 0;
+        int piece = 0, g = 0;
       bool ok = true;
       while (ok && pi.next(pc, a)) {
         const int steps = (pc.pe - pc.pa + 1) / 2;
@@ -470,6 +496,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               (i == 0 && piece > 0 && !wait_all(bar(kOFree), (piece - 1) & 1, ctl))) {
             ok = false;
             break;
+          }
+          if constexpr (kMixed) {
+            const uint32_t drop = reinterpret_cast<volatile uint32_t*>(drop_s[g & 3])[lane & 3];
+            if (__any_sync(0xffffffffu, drop)) {
+              if (!wait_all(bar(kFullV), g & 1, ctl) || !wait_all(bar(kFullV + 1), g & 1, ctl)) { ok = false; break; }
+              drop_values(sbase + kOffV, drop, lane);
+              if (lane < 4) drop_s[g & 3][lane] = 0;
+              __syncwarp();
+            }
           }
           tc_fence_after();
 #pragma unroll
@@ -581,16 +616,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) arrive_cta0(rank, bar(kSFree), sfree0);
         const int t0 = __shfl_sync(0xffffffffu, ref.page, 2 * (i & 15) + hh) * kPage + 32 * c;
+        const int seq = kShared ? __shfl_sync(0xffffffffu, ref.seq, 2 * (i & 15) + hh) : 0;
         uint32_t see = 0;
-        if constexpr (kShared) {
-          const int seq = __shfl_sync(0xffffffffu, ref.seq, 2 * (i & 15) + hh);
-          if (p < pc.pe) see = seq < 0 ? below(k.sight.prefix_end - t0) : seq == k.sight.seq ? below(k.sight.end - t0) : 0u;
-        } else if (p < pc.pe) {
-          see = below(k.sight.end - t0) & (below(a.sinks - t0) | ~below(k.sight.from - t0));
+        if (p < pc.pe) {
+          if constexpr (kShared)
+            see = seq < 0 ? below(k.sight.prefix_end - t0) : seq == k.sight.seq ? below(k.sight.end - t0) : 0u;
+          else
+            see = below(k.sight.end - t0) & (below(a.sinks - t0) | ~below(k.sight.from - t0));
         }
         const uint64_t s2 = f2_pack(scale2, scale2);
 #pragma unroll
         for (int j = 0; j < 32; j += 2) f2_unpack(f2_mul(f2_pack(y[j], y[j + 1]), s2), y[j], y[j + 1]);
+        bool dropped = false;
+        if (kMixed && (a.s_q > 1 || seq >= 0)) {
+          const uint32_t d = __reduce_or_sync(0xffffffffu, nonfinite_seen(y, see));
+          dropped = d != 0;
+          if (dropped && lane == 0) red_or_cluster(map_to_rank(smem_u32(&drop_s[gs & 3][2 * hh + c]), 0), d);
+        }
         if (!__all_sync(0xffffffffu, see == 0xffffffffu)) {
 #pragma unroll
           for (int j = 0; j < 32; ++j) y[j] = ((see >> j) & 1u) ? y[j] : -INFINITY;
@@ -653,7 +695,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         fence_proxy_async();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_cta0(rank, bar(kPFull), pfull0);
+        if (lane == 0) {
+          if (dropped) mbar_arrive_cluster(pfull0);  // with what it wrote to CTA 0
+          else arrive_cta0(rank, bar(kPFull), pfull0);
+        }
       }
       if (!ok) break;
       const int ge = g + steps - 1;
@@ -709,22 +754,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 }
 
-template <bool kShared>
+template <bool kShared, bool kMixed>
 cudaError_t launch_pair(const TileArgs& a, cudaStream_t stream) {
   static bool done[64] = {};
-  cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void*>(decode_tile_pair_kernel<kShared>), kAlloc, done);
+  cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void*>(decode_tile_pair_kernel<kShared, kMixed>), kAlloc, done);
   if (e != cudaSuccess) return e;
   CUtensorMap kv_map, rope_map, q_map;
   if (!tile_maps(a, 64, kQSmemBoxes, &kv_map, &rope_map, &q_map)) return cudaErrorInvalidValue;
   const uint64_t limit_ns = (uint64_t)a.wait_limit * 1000000ull;
-  return launch_dependent(decode_tile_pair_kernel<kShared>, 2 * a.num_workers * (kShared ? 1 : a.groups), kThreads, kAlloc,
-                          stream, kv_map, rope_map, q_map, a, limit_ns);
+  return launch_dependent(decode_tile_pair_kernel<kShared, kMixed>, 2 * a.num_workers * (kShared ? 1 : a.groups), kThreads,
+                          kAlloc, stream, kv_map, rope_map, q_map, a, limit_ns);
 }
 
 }  // namespace
 
 cudaError_t launch_decode_tile_pair(const TileArgs& a, cudaStream_t stream) {
-  return a.prefix_len ? launch_pair<true>(a, stream) : launch_pair<false>(a, stream);
+  if (a.prefix_len) return mixed_pages<true>(a) ? launch_pair<true, true>(a, stream) : launch_pair<true, false>(a, stream);
+  return mixed_pages<false>(a) ? launch_pair<false, true>(a, stream) : launch_pair<false, false>(a, stream);
 }
 
 }  // namespace mla

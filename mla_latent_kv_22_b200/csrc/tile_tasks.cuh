@@ -87,34 +87,44 @@ __device__ __forceinline__ int task_pages(const TileArgs& a, int t) {
 }
 
 struct Task {
-  Span s;          // window: the sequence's; shared: the prefix's (T and n alone)
+  // Window: the sequence's span, T and the hole as far as the tile's queries see; shared: the
+  // prefix's T (as far as they see) and n alone.
+  Span s;
   int b0, b1;      // the sequence; shared: the first and last with rows in the tile
   int row0, live;  // first query row of the whole batch's, rows of the tile
   int srow;        // window: row0 within its sequence
+  int cut;         // shared: the last tokens of b1 that none of its queries in the tile sees
 };
 
 template <int N, bool kShared>
 __device__ __forceinline__ Task load_task(const TileArgs& a, int t, int g) {
   Task k;
   if constexpr (kShared) {
-    k.s = Span{*a.prefix_len, prefix_pages(a), 0, 0, 0, 0};
     k.b0 = tile_seq0(a, t);
     k.b1 = tile_seq1(a, t);
     k.row0 = t * N;
     k.live = min(N, a.batch * a.rows - k.row0);
     k.srow = 0;
+    k.cut = a.s_q - 1 - (k.row0 + k.live - 1 - k.b1 * a.rows) / a.heads;
+    const int P = *a.prefix_len;
+    // Every sequence but the last has its last query in the tile, which sees the whole prefix.
+    k.s = Span{k.b0 < k.b1 ? P : min(P, P + a.seqlens[k.b1] - k.cut), prefix_pages(a), 0, 0, 0, 0};
   } else {
-    k.s = window_span(a, a.seqlens[t]);
-    k.b0 = k.b1 = t;
     k.srow = g * N;
     k.row0 = t * a.rows + k.srow;
     k.live = min(N, a.rows - k.srow);
+    k.s = window_span(a, a.seqlens[t]);
+    const int end = k.s.T - a.s_q + 1;  // of query 0
+    k.s.hole1 = max(0, end + k.srow / a.heads - a.window);
+    k.s.T = end + (k.srow + k.live - 1) / a.heads;
+    k.b0 = k.b1 = t;
+    k.cut = 0;
   }
   return k;
 }
 
 // A page of a task's list: its sequence (-1: the prefix), its index in that table, and the
-// tokens of the sequence (or prefix).
+// tokens of the sequence (or prefix) as far as the tile's queries see.
 struct PageRef {
   int seq, page, T;
   __device__ __forceinline__ int valid_rows() const { return min(max(T - page * kPage, 0), kPage); }
@@ -122,7 +132,7 @@ struct PageRef {
 
 // Page q of the own pages of sequences b0..b1 for every lane of a warp (each its own q; q < 0:
 // page q + prefix of the prefix, whose length is T).
-static __device__ __noinline__ PageRef page_ref_shared(const TileArgs& a, int q, int prefix, int T0, int b0, int b1) {
+static __device__ __noinline__ PageRef page_ref_shared(const TileArgs& a, int q, int prefix, int T0, int b0, int b1, int cut) {
   const int lane = threadIdx.x & 31;
   PageRef r{-1, q + prefix, T0};
   bool open = q >= 0;
@@ -145,7 +155,7 @@ static __device__ __noinline__ PageRef page_ref_shared(const TileArgs& a, int q,
       if (__shfl_sync(0xffffffffu, end, j + o - 1) <= q) j += o;
     const int first = __shfl_sync(0xffffffffu, end - n, j), Tj = __shfl_sync(0xffffffffu, T, j);
     if (open && q < total) {
-      r = PageRef{b0 + j, q - first, Tj};
+      r = PageRef{b0 + j, q - first, Tj - (b0 + j == b1 ? cut : 0)};
       open = false;
     }
     q -= total;
@@ -155,7 +165,7 @@ static __device__ __noinline__ PageRef page_ref_shared(const TileArgs& a, int q,
 // Page p of a task's list for every lane of a warp (each its own p, inside the list).
 template <bool kShared>
 __device__ __forceinline__ PageRef page_ref(const TileArgs& a, const Task& k, int p) {
-  if constexpr (kShared) return page_ref_shared(a, p - k.s.n, k.s.n, k.s.T, k.b0, k.b1);
+  if constexpr (kShared) return page_ref_shared(a, p - k.s.n, k.s.n, k.s.T, k.b0, k.b1, k.cut);
   else return {k.b0, k.s.real(p), k.s.T};
 }
 
@@ -171,16 +181,13 @@ template <bool kShared>
 __device__ __forceinline__ RowSight row_sight(const TileArgs& a, const Task& k, int row) {
   RowSight r{-2, -1, 0, -1, false};  // a row past the tile's sees nothing
   if (row >= k.live) return r;
+  r.seq = kShared ? (k.row0 + row) / a.rows : k.b0;
+  const int T = a.seqlens[r.seq];
+  r.end = T - a.s_q + 1 + (k.row0 + row - r.seq * a.rows) / a.heads;
   if constexpr (kShared) {
-    const int n = k.row0 + row;
-    r.seq = n / a.rows;
-    const int T = a.seqlens[r.seq];
     r.bad = bad_length(T, a.max_blocks);
-    r.end = T - a.s_q + 1 + (n - r.seq * a.rows) / a.heads;
-    r.prefix_end = min(k.s.T, k.s.T + r.end);
+    r.prefix_end = *a.prefix_len + min(r.end, 0);
   } else {
-    r.seq = k.b0;
-    r.end = k.s.T - a.s_q + 1 + (k.srow + row) / a.heads;
     r.from = r.end - a.window;
   }
   return r;
@@ -318,6 +325,44 @@ struct PieceLoads {
     rows = __shfl_sync(0xffffffffu, ref.valid_rows(), p - at);
   }
 };
+
+// Whether a call has pages that some rows of a tile see and others do not: several queries, or
+// tiles that hold rows of several sequences.  A hidden token's P is 0 for the rows that do not
+// see it, which its values survive only if they are finite: see nonfinite_seen.
+template <bool kShared>
+__host__ __device__ __forceinline__ bool mixed_pages(const TileArgs& a) {
+  return a.s_q > 1 || (kShared && a.rows % a.row_tile != 0);
+}
+
+// The tokens (bits) whose score is not finite in a row that sees them: a value that is not
+// finite makes its token's score so in every row.  (So does a query: the values themselves
+// are looked at, by finite_chunk, before they are taken as zeros.  The rows that see such a
+// token have no finite result anyway, or, at a score of -inf, weigh it by 0.)
+__device__ __forceinline__ uint32_t nonfinite_seen(const float (&y)[32], uint32_t see) {
+  uint64_t z = f2_pack(0.f, 0.f);
+  const uint64_t zero = z;
+#pragma unroll
+  for (int j = 0; j < 32; j += 2) z = f2_fma(f2_pack(y[j], y[j + 1]), zero, z);
+  float z0, z1;
+  f2_unpack(z, z0, z1);
+  uint32_t bits = 0;
+  if (z0 + z1 != 0.f) {  // NaN: some score is not finite
+#pragma unroll
+    for (int j = 0; j < 32; ++j) bits |= isfinite(y[j]) ? 0u : 1u << j;
+  }
+  return bits & see;
+}
+
+// A chunk of eight bf16 values with zeros for those that are not finite.
+__device__ __forceinline__ uint4 finite_chunk(uint4 v) {
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if ((w[i] & 0x7f80u) == 0x7f80u) w[i] &= 0xffff0000u;
+    if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] &= 0xffffu;
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
 
 // Bits [0, x) of a word.
 __device__ __forceinline__ uint32_t below(int x) { return x <= 0 ? 0u : x >= 32 ? 0xffffffffu : (1u << x) - 1u; }
