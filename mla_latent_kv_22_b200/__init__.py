@@ -81,6 +81,12 @@ def _load() -> ctypes.CDLL:
 
 lib = _load()
 
+try:
+    from . import _binding  # the quick path of the short calls (csrc/binding.cpp)
+except ImportError as e:
+    raise ImportError(f"the compiled binding is missing or does not load ({e}): build it with "
+                      "`python mla_latent_kv_22_b200/build.py`") from e
+
 
 def _check(status: int) -> None:
     if status != 0:
@@ -212,6 +218,8 @@ def mla_absorb_o(out_latent, w_uv, out, stream=None) -> None:
     """out[b,h] = bf16(out_latent[b,h]) W_UV[h] (fp32 accumulate, fp32 out).  out_latent is
     mla_decode's fp32, or the bf16 of mla_decode_window and mla_decode_shared (then
     mla_absorb_o_bf16 of the C ABI runs)."""
+    if stream is None and _quick(_binding.absorb_o(out_latent, w_uv, out)):
+        return
     B, H = int(out_latent.shape[0]), int(out_latent.shape[1])
     if out_latent.dtype == torch.bfloat16:
         dev = torch.cuda.current_device()
@@ -223,6 +231,17 @@ def mla_absorb_o(out_latent, w_uv, out, stream=None) -> None:
     _need(w_uv, "w_uv", torch.bfloat16, (H, D_LATENT, D_V))
     _need(out, "out", torch.float32, (B, H, D_V))
     _check(lib.mla_absorb_o(out_latent.data_ptr(), w_uv.data_ptr(), out.data_ptr(), B, H, _stream(stream)))
+
+
+def _quick(status) -> bool:
+    """Whether the compiled binding made the call (raising what the library reported); if it
+    did not, the arguments are for the code that follows to accept or to refuse."""
+    if status is None:
+        return True
+    if status is NotImplemented:
+        return False
+    _check(status)
+    return True
 
 
 def _here(t, name, dtype, shape, dev: int) -> int:
@@ -273,6 +292,9 @@ def mla_append(c_kv, k_rope, kv_cache, block_table, cache_seqlens, cos_sin, cu_t
     block_table as in mla_decode; cache_seqlens [B] int32, lengths with the new tokens;
     cos_sin [max_pos,64] fp32; cu_tokens [B+1] int32, or None for N / B tokens per
     sequence; pos_offset [B] int32 or None."""
+    if stream is None and _quick(_binding.append(c_kv, k_rope, kv_cache, block_table, cache_seqlens, cos_sin, cu_tokens, q_rope,
+                                                 q_out, pos_offset, interleaved)):
+        return
     if c_kv.dim() != 2:
         raise ValueError("c_kv must be [N, 512]")
     dev = torch.cuda.current_device()
@@ -329,6 +351,9 @@ def mla_decode_window(q, kv_cache, block_table, cache_seqlens, out, lse, softmax
     arguments are those of mla_decode.  ``workspace``: a CUDA uint8 tensor of at least
     mla_decode_window_workspace_size(B, s_q, H) bytes, or None to take one from torch's
     allocator for this call."""
+    if workspace is None and stream is None and _quick(_binding.decode_window(
+            q, kv_cache, block_table, cache_seqlens, out, lse, softmax_scale, window, sinks)):
+        return
     (B, SQ, H), rows = _query_shape(q)
     dev = torch.cuda.current_device()
     p_q = _here(q, "q", torch.bfloat16, rows + (D_QK,), dev)
@@ -351,6 +376,9 @@ def mla_decode_shared(q, kv_cache, prefix_table, prefix_len, block_table, cache_
     [prefix_blocks] int32 and prefix_len [1] int32 describe it, block_table
     [B,max_blocks] and cache_seqlens [B] int32 each sequence's own tokens; q, out, lse,
     workspace as in mla_decode_window (mla_decode_shared_workspace_size)."""
+    if workspace is None and stream is None and _quick(_binding.decode_shared(
+            q, kv_cache, prefix_table, prefix_len, block_table, cache_seqlens, out, lse, softmax_scale)):
+        return
     (B, SQ, H), rows = _query_shape(q)
     dev = torch.cuda.current_device()
     p_q = _here(q, "q", torch.bfloat16, rows + (D_QK,), dev)

@@ -1,4 +1,5 @@
-"""Builds libmla.so in-tree with nvcc for sm_100a (B200).
+"""Builds libmla.so in-tree with nvcc for sm_100a (B200), and _binding.so, the binding's
+quick path, with g++ against torch's headers.
 
     python mla_latent_kv_22_b200/build.py [--force] [--verbose] [--ptxas]
 
@@ -11,12 +12,15 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmla.so")
+BINDING = os.path.join(PKG, "_binding.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -36,11 +40,16 @@ def _deps() -> list[str]:
         glob.glob(os.path.join(INCLUDE, "*.h"))
 
 
+def _newer(target: str, deps: list[str]) -> bool:
+    return os.path.exists(target) and all(os.path.getmtime(p) <= os.path.getmtime(target) for p in deps)
+
+
+def _binding_up_to_date() -> bool:
+    return _newer(BINDING, [BINDING_SRC] + glob.glob(os.path.join(INCLUDE, "*.h")))
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
-        return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    return _newer(LIB, _deps()) and _binding_up_to_date()
 
 
 def nvcc() -> str:
@@ -50,20 +59,36 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
-def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
-    if not force and up_to_date():
-        return LIB
-    tmp = LIB + ".tmp"
-    cmd = [nvcc(), *NVCC_FLAGS, *(extra or []), "-I", INCLUDE, "-I", CSRC, "-o", tmp, *sources()]
+def _run(cmd: list[str], target: str, verbose: bool) -> None:
+    """Runs a compiler whose output goes to target + ".tmp", then moves it into place."""
     if verbose:
         print(" ".join(cmd))
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         sys.stderr.write(r.stdout + r.stderr)
-        raise RuntimeError("nvcc failed building libmla.so")
+        raise RuntimeError(f"{cmd[0]} failed building {os.path.basename(target)}")
     if verbose and (r.stdout or r.stderr):
         print(r.stdout + r.stderr)
-    os.replace(tmp, LIB)
+    os.replace(target + ".tmp", target)
+
+
+def _build_binding(verbose: bool) -> None:
+    import torch
+
+    T = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          "-I", INCLUDE, "-isystem", os.path.join(T, "include"), "-isystem", os.path.join(T, "include/torch/csrc/api/include"),
+          "-isystem", sysconfig.get_paths()["include"], "-isystem", cuda, "-o", BINDING + ".tmp", BINDING_SRC, "-L", PKG, "-l:libmla.so",
+          "-L", os.path.join(T, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+          "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + os.path.join(T, "lib")], BINDING, verbose)
+
+
+def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
+    if force or not _newer(LIB, _deps()):
+        _run([nvcc(), *NVCC_FLAGS, *(extra or []), "-I", INCLUDE, "-I", CSRC, "-o", LIB + ".tmp", *sources()], LIB, verbose)
+    if force or not _binding_up_to_date():
+        _build_binding(verbose)
     return LIB
 
 

@@ -6,6 +6,7 @@ import os
 import re
 
 import pytest
+import torch
 
 import mla_latent_kv_22_b200 as M
 
@@ -153,3 +154,13 @@ def test_append_host_validation(kw, status):
 ])
 def test_absorb_o_bf16_host_validation(args, status):
     assert M.lib.mla_absorb_o_bf16(*args) == status
+
+
+def test_the_quick_binding_hands_back_what_does_not_fit():
+    t = torch.zeros(1, 16, 576)
+    for fn, n in ((M._binding.decode_window, 9), (M._binding.decode_shared, 9), (M._binding.append, 11), (M._binding.absorb_o, 3)):
+        assert fn() is NotImplemented
+        assert fn(*[None] * n) is NotImplemented
+        assert fn(*[t] * n) is NotImplemented          # CPU tensors
+        assert fn(*["text"] * n) is NotImplemented
+        assert fn(*[t.bfloat16()] * n) is NotImplemented
