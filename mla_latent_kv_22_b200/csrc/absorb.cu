@@ -491,21 +491,25 @@ __global__ void __launch_bounds__(kOThreads, 1)
 // out[b,h,:] = x[b,h,:] W_UV[h] with x already bf16 (the window and shared-prefix decodes'
 // output), taken transposed: D = out^T[128 v x N rows], A = W_UV[h]^T (MN-major boxes of
 // [64 k x 64 v]), B = x (K-major, N batch rows).  Bound by HBM (W_UV and x once): with the
-// batch as N, a short batch costs no padding, and chunks of 64 k (16 KB of W_UV and N rows
-// of x) run through one ring across items, so one item's loads fly under the previous
-// one's MMAs and stores.  An item is a head, a tile of N batch rows (16 to 128) and, when
-// there are too few heads to give every SM one, one half of the 128 v dims (kHalf: M = 64).
+// batch as N, a short batch costs no padding, and chunks of 256 k (128 where the rows of x
+// need the room) run through one ring across items, so one item's loads fly under the
+// previous one's MMAs and stores.  A chunk is two TMA boxes, one of W_UV and one of x: a
+// thread issues a box in 250 to 480 cycles whatever its size, and in boxes of 64 x 64 the
+// calls took 4.7, 4.9 and 8.1 us for 5 x 16, 64 x 16 and 64 x 128 rows x heads, against 2.9,
+// 3.5 and 7.4 (operands not in L2).  An item is a head, a tile of N batch rows (16 to 128)
+// and, when there are too few heads to give every SM one, one half of the 128 v dims (kHalf:
+// M = 64).
 constexpr int kXThreads = 192;
 constexpr int kXW = 16384;           // 64 k x 128 v of W_UV
-constexpr int kXMaxStages = 11;
+constexpr int kXMaxStages = 5;
 constexpr int kXSmem = 229376;
-constexpr int kXChunks = kDLatent / 64;
+constexpr int kXBlocks = kDLatent / 64;
 enum XBar { kXFull = 0, kXEmpty = kXFull + kXMaxStages, kXDFull = kXEmpty + kXMaxStages, kXDEmpty = kXDFull + 2, kXDone = kXDEmpty + 2, kXNumBars };
 
 template <bool kHalf>
 __global__ void __launch_bounds__(kXThreads, 1)
     absorb_o_bf16_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
-                         float* __restrict__ out, int B, int H, int N, int stages, int* err, uint64_t limit_ns) {
+                         float* __restrict__ out, int B, int H, int N, int kc, int stages, int* err, uint64_t limit_ns) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[kXNumBars];
   __shared__ uint32_t tmem_s;
@@ -516,7 +520,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int kParts = kHalf ? 2 : 1, kM = 128 / kParts;
   constexpr int kWBytes = kXW / kParts;
-  const int stage_bytes = kWBytes + N * 128;
+  const int stage_bytes = kc * (kWBytes + N * 128);  // kc blocks of 64 k
   const int items = H * kParts * ((B + N - 1) / N);
 
   if (tid == 0) {
@@ -554,12 +558,12 @@ __global__ void __launch_bounds__(kXThreads, 1)
       bool ok = true;
       for (int item = blockIdx.x; ok && item < items; item += gridDim.x) {
         const int hp = item % (H * kParts), h = hp / kParts, v0 = kM * (hp % kParts), b0 = (item / (H * kParts)) * N;
-        for (int c = 0; c < kXChunks; ++c) {
+        for (int c = 0; c < kXBlocks; c += kc) {
           if (!wait_on(bar(kXEmpty + s), phase ^ 1, gd)) { ok = false; break; }
           const uint32_t st = sbase + s * stage_bytes;
           mbar_expect_tx(bar(kXFull + s), stage_bytes);
-          for (int v = 0; v < kM; v += 64) tma_load_3d(st + v * 128, &map_w, v0 + v, 64 * c, h, bar(kXFull + s));
-          tma_load_3d(st + kWBytes, &map_x, 64 * c, h, b0, bar(kXFull + s));
+          tma_load_4d(st, &map_w, 0, 64 * c, v0 / 64, h, bar(kXFull + s));
+          tma_load_4d(st + kc * kWBytes, &map_x, 0, b0, c, h, bar(kXFull + s));
           ++issued;
           if (++s == stages) {
             s = 0;
@@ -577,19 +581,23 @@ __global__ void __launch_bounds__(kXThreads, 1)
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issue
     const uint32_t idesc = idesc_bf16_f32(kM, N, 1, 0);
-    constexpr uint64_t kKMajor = desc_sw128_const(16, 1024), kMNMajor = desc_sw128_const(8192, 1024);
+    // W_UV: the two 64-v halves of a chunk lie kc blocks apart.
+    constexpr uint64_t kKMajor = desc_sw128_const(16, 1024);
+    const uint64_t mn_major = desc_sw128(0, kc * 8192, 1024);
     int s = 0, it = 0;
     uint32_t phase = 0;
     bool ok = true;
     for (int item = blockIdx.x; ok && item < items; item += gridDim.x, ++it) {
       const int d = it & 1;
       ok = __all_sync(0xffffffffu, wait_on(bar(kXDEmpty + d), ((it >> 1) & 1) ^ 1, gd));
-      for (int c = 0; ok && c < kXChunks; ++c) {
+      for (int c = 0; ok && c < kXBlocks; c += kc) {
         ok = __all_sync(0xffffffffu, wait_on(bar(kXFull + s), phase, gd));
         if (!ok) break;
         tc_fence_after();
         const uint32_t st = sbase + s * stage_bytes;
-        mma_x4_elect<128, 2>(tmem + d * 128, kMNMajor | desc_addr(st), kKMajor | desc_addr(st + kWBytes), idesc, c > 0);
+        for (int j = 0; j < kc; ++j)
+          mma_x4_elect<128, 2>(tmem + d * 128, mn_major | desc_addr(st + j * 8192),
+                               kKMajor | desc_addr(st + kc * kWBytes + j * N * 128), idesc, c + j > 0);
         mma_commit_elect(bar(kXEmpty + s));
         if (++s == stages) {
           s = 0;
@@ -738,15 +746,15 @@ cudaError_t launch_absorb_o(const float* out_latent, const __nv_bfloat16* w_uv, 
 
 template <bool kHalf>
 static cudaError_t launch_absorb_o_bf16_as(const CUtensorMap& mx, const CUtensorMap& mw, float* out, int batch, int heads,
-                                           int rows, int* err, cudaStream_t stream) {
+                                           int rows, int kc, int* err, cudaStream_t stream) {
   static bool done[64] = {};
   cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void*>(absorb_o_bf16_kernel<kHalf>), kXSmem + 1024, done);
   if (e != cudaSuccess) return e;
   const int parts = kHalf ? 2 : 1;
   const int items = heads * parts * ((batch + rows - 1) / rows);
-  const int fit = kXSmem / (kXW / parts + rows * 128), stages = fit < kXMaxStages ? fit : kXMaxStages;
+  const int stage = kc * (kXW / parts + rows * 128), fit = kXSmem / stage, stages = fit < kXMaxStages ? fit : kXMaxStages;
   return launch_dependent(absorb_o_bf16_kernel<kHalf>, items < sm_count() ? items : sm_count(), kXThreads, kXSmem + 1024,
-                          stream, mx, mw, out, batch, heads, rows, stages, err, 2000ull * 1000000ull);
+                          stream, mx, mw, out, batch, heads, rows, kc, stages, err, 2000ull * 1000000ull);
 }
 
 cudaError_t launch_absorb_o_bf16(const __nv_bfloat16* out_latent, const __nv_bfloat16* w_uv, float* out, int batch,
@@ -756,14 +764,27 @@ cudaError_t launch_absorb_o_bf16(const __nv_bfloat16* out_latent, const __nv_bfl
   const auto bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
   const int rows = batch <= 16 ? 16 : batch <= 32 ? 32 : batch <= 64 ? 64 : 128;
-  if (!map3d(&mx, bf, out_latent, kDLatent, H, Bn, kDLatent * 2, H * kDLatent * 2, 64, 1, rows, sw) ||
-      !map3d(&mw, bf, w_uv, MLA_D_V, kDLatent, H, MLA_D_V * 2, (uint64_t)kDLatent * MLA_D_V * 2, 64, 64, 1, sw))
-    return cudaErrorInvalidValue;
   // Half items when even they leave SMs without one: the loads of an item (128 KB of W_UV)
   // are then shared by two SMs.
   const int items = heads * ((batch + rows - 1) / rows);
-  return 2 * items <= sm_count() ? launch_absorb_o_bf16_as<true>(mx, mw, out, batch, heads, rows, err, stream)
-                                 : launch_absorb_o_bf16_as<false>(mx, mw, out, batch, heads, rows, err, stream);
+  const bool half = 2 * items <= sm_count();
+  // The longest chunk of which two fit.
+  const int kc = 2 * 4 * ((half ? kXW / 2 : kXW) + rows * 128) <= kXSmem ? 4 : 2;
+  // x as [8 blocks of 64 k][batch][64 k] of a head, W_UV as [2 halves of 64 v][512 k][64 v].
+  const auto enc = encoder();
+  if (!enc) return cudaErrorNotSupported;
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  auto map4d = [&](CUtensorMap* m, const __nv_bfloat16* p, const cuuint64_t (&dims)[4], const cuuint64_t (&strides)[3],
+                   const cuuint32_t (&box)[4]) {
+    return enc(m, bf, 4, const_cast<__nv_bfloat16*>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  if (!map4d(&mx, out_latent, {64, Bn, 8, H}, {H * kDLatent * 2, 128, kDLatent * 2}, {64, (cuuint32_t)rows, (cuuint32_t)kc, 1}) ||
+      !map4d(&mw, w_uv, {64, kDLatent, 2, H}, {MLA_D_V * 2, 128, (cuuint64_t)kDLatent * MLA_D_V * 2},
+             {64, 64 * (cuuint32_t)kc, half ? 1u : 2u, 1}))
+    return cudaErrorInvalidValue;
+  return half ? launch_absorb_o_bf16_as<true>(mx, mw, out, batch, heads, rows, kc, err, stream)
+              : launch_absorb_o_bf16_as<false>(mx, mw, out, batch, heads, rows, kc, err, stream);
 }
 
 }  // namespace mla
