@@ -326,12 +326,14 @@ typedef enum {
                                    above the split quota, else split; 1 = always split;
                                    2 = whole sequences whenever batch <= the worker count.
                                    A forced MLA_KNOB_NUM_WORKERS always splits.             */
-  MLA_KNOB_PIECE_COST = 6       /* pages a split charges each sequence for its fixed cost
+  MLA_KNOB_PIECE_COST = 6,      /* pages a split charges each sequence for its fixed cost
                                    (q' staging, pipeline fill, epilogue) when it lays the
                                    sequences end to end and cuts equal shares: 0 = auto (8,
                                    a multiple of the 4-page step, so pieces of step-aligned
                                    sequences stay aligned); k > 0: min(k - 1, 256) pages 
                                    (1 = split by pages alone)                               */
+  MLA_KNOB_ROW_TILE = 7         /* query rows per tile of mla_decode_window and _shared: 16,
+                                   32 or 128; any other value = auto                        */
 } mla_knob_t;
 mla_status_t mla_set_knob(mla_knob_t knob, int value);
 int mla_get_knob(mla_knob_t knob);

@@ -30,7 +30,7 @@ STATUS = {
     5: "MLA_ERR_DEVICE_BAD_PAGE", 6: "MLA_ERR_DEVICE_TIMEOUT", 7: "MLA_ERR_DEVICE_BAD_POSITION",
 }
 KNOB = {"num_workers": 0, "min_pages": 1, "decode_kernel": 2, "wait_limit": 3, "withhold_arrive": 4, "split_policy": 5,
-        "piece_cost": 6}
+        "piece_cost": 6, "row_tile": 7}
 
 D_LATENT, D_ROPE, D_QK, PAGE, D_NOPE, D_V, MAX_HEADS = 512, 64, 576, 64, 128, 128, 128
 

@@ -488,7 +488,7 @@ size_t tile_workspace(int batch, int s_q, int heads, bool shared) {
   a.batch = batch;
   a.rows = s_q * heads;
   a.prefix_len = shared ? &some : nullptr;
-  return plan_tile(&a, d->sm_count, g_knobs[MLA_KNOB_NUM_WORKERS].load(), nullptr);
+  return tile_bytes(a, d->sm_count, g_knobs[MLA_KNOB_NUM_WORKERS].load());
 }
 
 // The checks and launch common to both; `a` holds the call's arguments.

@@ -1,22 +1,24 @@
 // Sliding-window and shared-prefix decode: split-KV absorbed decode with one CTA per
-// worker, a tile of N = 16, 32 or 64 query rows and one 64-token page per step.
+// worker, a tile of N = 16 or 32 query rows and one 64-token page per step.
 //
 // A page is loaded once and feeds both products from the same shared memory:
 //     S[64 x 64]    = q'[N x 576] . K^T       (M = 64 rows, N = 64 tokens, K = 576)
 //     O^T[512 x N] += V^T[512 x 64] . P^T     (four M = 128 blocks of dims, N rows, K = 64)
 // The second product is taken transposed: its accumulator is 4 N columns of tensor memory
-// instead of 512, so it fits beside S, and the page's [64 tokens x 64 dims] boxes serve as
-// the K-major B operand of the first and, read MN-major, as the A operand of the second.
-// Rows of S at or beyond N come from whatever shared memory follows q' and are never read.
+// instead of 512, so two of them fit beside S, and the page's [64 tokens x 64 dims] boxes
+// serve as the K-major B operand of the first and, read MN-major, as the A operand of the
+// second.  Rows of S at or beyond N come from whatever shared memory follows q' and are
+// never read.
 //
-// Every 64-token page costs 36 + 16 MMAs whatever the row count, under the time its 73.7 KB
-// take from HBM at 148 SMs' share of the copy rate; so few rows (a window decode on a
-// tensor-parallel shard) run at the speed of the loads, and the rows of many sequences are
-// packed into tiles of 64 where they share the tokens (a common prefix).
+// Every 64-token page costs 36 + 16 MMAs whatever the row count (32 and 39-40 cycles each,
+// bound by shared memory's 128 bytes a cycle: 1,780 cycles) under the 3,300 that its 73.7 KB
+// take from HBM at an SM's share of the copy rate; so few rows (a window decode on a
+// tensor-parallel shard) run at the speed of the loads: 1,700 ns a page on all 148 SMs, 6.4
+// TB/s.  More rows share pages in tiles of 128 on a CTA pair (decode_tile_pair.cu).
 //
 // Roles (384 threads).  Warps 0-3: softmax of the 16 rows in their TMEM quadrant (two threads
-// per row, 32 tokens each).  Warps 4-7: store a piece's O, with up to 32 rows from a second
-// accumulator while the next piece runs.  Warp 8: page loads (TMA), two 32 KB halves of 256
+// per row, 32 tokens each).  Warps 4-7: store a piece's O, from one of two accumulators
+// while the next piece runs in the other.  Warp 8: page loads (TMA), two 32 KB halves of 256
 // latent dims per page into a ring, freed by the second product, and the rope dims into two
 // 8 KB slots, freed by the first.  Warp 9: q' loads and the first product's MMAs.  Warp 10:
 // zeroes the rows of a page that no query of the sequence sees (past its end, or between the
@@ -38,6 +40,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <cmath>
 
 #include "mla_device.cuh"
 #include "mla_internal.h"
@@ -64,16 +67,16 @@ template <int N>
 struct Layout {
   static constexpr int kQBox = N * 128;
   static constexpr int kQBufs = N == 16 ? 2 : 1;
-  static constexpr int kPBufs = N == 64 ? 1 : 2;
-  static constexpr int kOBufs = N == 64 ? 1 : 2;  // O^T accumulators: a piece's leaves under the next one's pages
-  static constexpr int kSlots = N == 64 ? 4 : 5;
+  static constexpr int kPBufs = 2;
+  static constexpr int kOBufs = 2;  // O^T accumulators: a piece's leaves under the next one's pages
+  static constexpr int kSlots = 5;
   static constexpr int kOffQ = 0;
   static constexpr int kOffP = kQBufs * 9 * kQBox;
   static constexpr int kOffRope = kOffP + kPBufs * kQBox;
   static constexpr int kOffRing = kOffRope + 2 * kBox;
   static constexpr int kBytes = kOffRing + kSlots * kSlotBytes;
   static constexpr int kAlloc = kBytes + 1024;  // + alignment slack
-  static_assert(N == 16 || N == 32 || N == 64, "row tile");
+  static_assert(N == 16 || N == 32, "row tile");
   // The first product reads 64 rows of every q' box; the last box's reach stays inside.
   static_assert((kQBufs * 9 - 1) * kQBox + 64 * 128 <= kBytes, "q' rows read outside the allocation");
   static_assert(kQBox % 1024 == 0 && kOffRope % 1024 == 0 && kOffRing % 1024 == 0, "1024-byte tiles");
@@ -237,8 +240,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kWords = (N + 31) / 32;
   __shared__ uint32_t bad_s[8][kWords];  // [piece % 8] a bit for each row that a page id outside the cache spoils
   __shared__ RangeScratch range_s;
-  // Rescale factors and whether a warp has any.  Four pages deep (two with one P buffer): a
-  // warp may be that far ahead of another across the end of a piece, where they do not meet.
+  // Rescale factors and whether a warp has any.  Four pages deep: a warp may be three pages
+  // ahead of another across the end of a piece, where they do not meet.
   constexpr int kAhead = 2 * Lay::kPBufs;
   __shared__ float al_s[kAhead][N];       // [page % kAhead][row]
   __shared__ int need_s[kAhead][4];       // [page % kAhead][warp]
@@ -342,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             phase ^= 1u;
           }
         }
-        if (p == ld.pc.pa) ld.look();
+        if (p == min(ld.pc.pa + 1, ld.pc.pe - 1)) ld.look();
       }
       ++piece;
     }
@@ -608,12 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         // The page that last used this P buffer must have been read before it is rewritten.
-        if (Lay::kPBufs == 2) {
-          if (!wait_all(bar(kODone + u), ((gs >> 1) & 1) ^ 1, ctl)) { ok = false; break; }
-        } else if (gs > 0 && !wait_all(bar(kODone + (u ^ 1)), ((gs - 1) >> 1) & 1, ctl)) {
-          ok = false;
-          break;
-        }
+        if (!wait_all(bar(kODone + u), ((gs >> 1) & 1) ^ 1, ctl)) { ok = false; break; }
         if (holds) {
           l *= alpha;
           const float mm = m == -INFINITY ? 0.f : m;  // a row that has seen nothing holds only masked scores
@@ -703,19 +701,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---------------------------------------------------------------- combine
 // Merges the pieces of a row's task by their lse, in the order of their pages, and writes the
-// rows that no piece holds.  Four warps take a row, 128 dims each, and four pieces' loads are
-// in flight at a time, the first four before the weights are known (7 rows of 9 pieces ran
-// 4.5 us from serial loads).
-constexpr int kCombineThreads = 256, kCombineRows = kCombineThreads / 128, kCombineCtas = 6;  // per SM
+// rows that no piece holds.  Four warps take a row, 128 dims each, with four pieces' loads in
+// flight, the first four before the weights are known.  Where there are few rows, each of
+// kSplit = 4 such groups takes a quarter of the pieces, and the first adds them up in order
+// (a call of 30 rows in 148 pieces 30.4 -> 21.5 us).
+constexpr int kCombineThreads = 512;
 
-template <bool kShared>
-__global__ void __launch_bounds__(kCombineThreads, kCombineCtas) combine_tile_kernel(const __grid_constant__ TileArgs a) {
+template <bool kShared, int kSplit>
+__global__ void __launch_bounds__(kCombineThreads, 3) combine_tile_kernel(const __grid_constant__ TileArgs a) {
+  constexpr int kRows = kCombineThreads / (128 * kSplit);  // rows at a time
+  __shared__ float4 acc_s[kSplit][128];
+  __shared__ float wsum_s[kSplit][4];
   grid_dep_launch_dependents();
   grid_dep_wait();
-  const int lane = threadIdx.x & 31, part = (threadIdx.x >> 5) & 3;
+  const int lane = threadIdx.x & 31, part = (threadIdx.x >> 5) & 3, group = threadIdx.x >> 7;
+  const int split = kSplit > 1 ? group : 0;
   const int R = a.batch * a.rows, N = a.row_tile;
 #pragma unroll 1
-  for (int gr = blockIdx.x * kCombineRows + (threadIdx.x >> 7); gr < R; gr += gridDim.x * kCombineRows) {
+  for (int gr = blockIdx.x * kRows + (kSplit > 1 ? 0 : group); gr < R; gr += gridDim.x * kRows) {
     const int b = gr / a.rows, r = gr - b * a.rows;
     const SeqInfo s = a.task[kShared ? gr / N : b];
     bool nan = s.num_pieces < 0;
@@ -729,18 +732,19 @@ __global__ void __launch_bounds__(kCombineThreads, kCombineCtas) combine_tile_ke
     const size_t stride = kShared ? N : (size_t)a.groups * N;
     const int r0 = kShared ? gr % N : r;
     auto at = [&](int k) -> size_t { return (size_t)(k == 0 ? s.first_slot : s.first_worker + k) * stride + r0; };
+    // This group's pieces [ka, ke): whole fours.
+    const int per = kSplit > 1 ? ((n + 4 * kSplit - 1) / (4 * kSplit)) * 4 : n, ka = split * per, ke = min(n, ka + per);
     float4 x[4];
     auto load = [&](int k0) {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        x[j] = k0 + j < n ? reinterpret_cast<const float4*>(a.part_o + at(k0 + j) * kDLatent)[32 * part + lane]
-                          : make_float4(0.f, 0.f, 0.f, 0.f);
+        x[j] = k0 + j < ke ? reinterpret_cast<const float4*>(a.part_o + at(k0 + j) * kDLatent)[32 * part + lane]
+                           : make_float4(0.f, 0.f, 0.f, 0.f);
     };
-    load(0);
-    float mine = lane < n ? a.part_lse[at(lane)] : -INFINITY, L = mine;  // piece lane's, later its weight
-    nan |= mine != mine;
+    load(ka);
+    float L = -INFINITY;
 #pragma unroll 1
-    for (int k = lane + 32; k < n; k += 32) {
+    for (int k = lane; k < n; k += 32) {
       const float v = a.part_lse[at(k)];
       nan |= v != v;
       L = fmaxf(L, v);
@@ -749,21 +753,21 @@ __global__ void __launch_bounds__(kCombineThreads, kCombineCtas) combine_tile_ke
     for (int o = 16; o; o >>= 1) L = fmaxf(L, __shfl_xor_sync(0xffffffffu, L, o));
     uint2* const out2 = reinterpret_cast<uint2*>(a.out + (size_t)gr * kDLatent) + 32 * part + lane;
     nan = __any_sync(0xffffffffu, nan);
-    if (nan || L == -INFINITY) {
+    if (nan || L == -INFINITY) {  // alike in all groups of a row
       const uint32_t v = nan ? 0x7fff7fffu : 0u;
-      *out2 = make_uint2(v, v);
-      if (part == 0 && lane == 0) a.lse[gr] = nan ? NAN : -INFINITY;
+      if (split == 0) *out2 = make_uint2(v, v);
+      if (split == 0 && part == 0 && lane == 0) a.lse[gr] = nan ? NAN : -INFINITY;
       continue;
     }
-    mine = expf(mine - L);
-    float acc[4] = {0.f, 0.f, 0.f, 0.f}, wsum = 0.f;
+    float acc[4] = {0.f, 0.f, 0.f, 0.f}, wsum = 0.f, mine = 0.f;
 #pragma unroll 1
-    for (int k0 = 0; k0 < n; k0 += 4) {
-      if (k0) load(k0);
-      if (k0 && (k0 & 31) == 0) mine = k0 + lane < n ? expf(a.part_lse[at(k0 + lane)] - L) : 0.f;
+    for (int k0 = ka; k0 < ke; k0 += 4) {
+      if (k0 > ka) load(k0);
+      const int i = (k0 - ka) & 31;
+      if (i == 0) mine = k0 + lane < ke ? expf(a.part_lse[at(k0 + lane)] - L) : 0.f;  // the weights of 32 pieces
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float wk = __shfl_sync(0xffffffffu, mine, (k0 + j) & 31);  // 0 past the last piece
+        const float wk = __shfl_sync(0xffffffffu, mine, i + j);  // 0 past the last piece
         wsum += wk;
         acc[0] += wk * x[j].x;
         acc[1] += wk * x[j].y;
@@ -771,10 +775,34 @@ __global__ void __launch_bounds__(kCombineThreads, kCombineCtas) combine_tile_ke
         acc[3] += wk * x[j].w;
       }
     }
-    const float inv = 1.f / wsum;
-    *out2 = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
-    if (part == 0 && lane == 0) a.lse[gr] = L + logf(wsum);
+    if (kSplit > 1) {
+      acc_s[split][32 * part + lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      if (lane == 0) wsum_s[split][part] = wsum;
+      __syncthreads();
+      if (split == 0) {
+#pragma unroll
+        for (int g = 1; g < kSplit; ++g) {
+          const float4 y = acc_s[g][32 * part + lane];
+          acc[0] += y.x;
+          acc[1] += y.y;
+          acc[2] += y.z;
+          acc[3] += y.w;
+          wsum += wsum_s[g][part];
+        }
+      }
+      __syncthreads();
+    }
+    if (split == 0) {
+      const float inv = 1.f / wsum;
+      *out2 = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+      if (part == 0 && lane == 0) a.lse[gr] = L + logf(wsum);
+    }
   }
+}
+
+template <bool kShared, int kSplit>
+cudaError_t launch_combine_tile(const TileArgs& a, int grid, cudaStream_t stream) {
+  return launch_dependent(combine_tile_kernel<kShared, kSplit>, grid, kCombineThreads, 0, stream, a);
 }
 
 template <int N, bool kShared>
@@ -791,22 +819,22 @@ cudaError_t launch_tile(const TileArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-size_t plan_tile(TileArgs* a, int sm_count, int forced_workers, void* base) {
-  a->sm_count = sm_count;
+namespace {
+
+constexpr int kRowTiles[] = {16, 32, 128};
+
+// The sizes that follow from a row tile, and the workspace (see plan_tile).
+size_t lay_out(TileArgs* a, int row_tile, int sm_count, int forced_workers, void* base) {
   const bool shared = a->prefix_len != nullptr;
-  const long long R = (long long)a->batch * a->rows;
-  // Up to 64 rows, the narrowest tile that holds them on one CTA: narrow tiles leave more
-  // shared memory to the load ring.  More rows take tiles of 128 on a CTA pair.  A prefix
-  // is read by tiles of the whole batch's rows, so there the batch's rows count.
-  const long long all = shared ? R : a->rows;
-  a->row_tile = all <= 16 ? 16 : all <= 32 ? 32 : all <= 64 ? 64 : 128;
-  a->groups = (a->rows + a->row_tile - 1) / a->row_tile;
-  a->tiles = shared ? (int)((R + a->row_tile - 1) / a->row_tile) : 0;
-  const int workers = a->row_tile == 128 ? sm_count / 2 : sm_count;
+  a->sm_count = sm_count;
+  a->row_tile = row_tile;
+  a->groups = (a->rows + row_tile - 1) / row_tile;
+  a->tiles = shared ? (int)(((long long)a->batch * a->rows + row_tile - 1) / row_tile) : 0;
+  const int workers = row_tile == 128 ? sm_count / 2 : sm_count;
   a->num_workers = std::max(1, shared ? workers : workers / a->groups);
   if (forced_workers > 0) a->num_workers = forced_workers;
   const size_t tasks = shared ? a->tiles : a->batch;
-  const size_t rows = (size_t)2 * a->num_workers * (shared ? 1 : a->groups) * a->row_tile;
+  const size_t rows = (size_t)2 * a->num_workers * (shared ? 1 : a->groups) * row_tile;
   size_t off = 0;
   auto take = [&](size_t bytes) {
     char* p = base ? static_cast<char*>(base) + off : nullptr;
@@ -817,6 +845,56 @@ size_t plan_tile(TileArgs* a, int sm_count, int forced_workers, void* base) {
   a->part_lse = reinterpret_cast<float*>(take(rows * sizeof(float)));
   a->part_o = reinterpret_cast<float*>(take(rows * kDLatent * sizeof(float)));
   return off;
+}
+
+// The row tile with the least estimated time.  A narrow tile costs more per row and page, but
+// spreads the fixed parts of a short call (above all the partials' stores, at 32 bytes a cycle
+// and SM) over more SMs.  The pages are those that the window or the tables allow, half of the
+// own pages of a shared prefix.
+int pick_row_tile(const TileArgs& a, int sm_count) {
+  const int forced = knob_value(MLA_KNOB_ROW_TILE);
+  for (int n : kRowTiles)
+    if (forced == n) return n;
+  // us: of a call, and of a page per worker, fitted to 39 shapes (us at 16 / 32 / 128 rows a
+  // tile: a window of 512 for 128 heads 11.6 / 11.7 / 15.5, 64 windows of 1,024 for 64 heads
+  // 58 / 37 / 27; 7 sequences of 16 heads behind 1,000 tokens 13.4 / 14.2 / 17.5, 16 behind
+  // 16,000 44 / 32 / 25; tiles of 64 rows on one CTA were best nowhere).
+  const double fixed[] = {10.2, 10.8, 14.3}, page[] = {1.5, 1.7, 0.8};
+  const long long all = a.prefix_len ? (long long)a.batch * a.rows : a.rows;
+  double best = 0;
+  int tile = 0;
+  for (int i = 0; i < (all <= 16 ? 1 : 3); ++i) {
+    const int n = kRowTiles[i];
+    const double groups = (a.rows + n - 1) / n;
+    double pages;
+    if (a.prefix_len) {
+      pages = (double)((all + n - 1) / n) * a.prefix_blocks + 0.5 * a.batch * a.max_blocks * (1 + (a.rows - 1) / n);
+    } else {
+      const double most = ((double)a.window + a.s_q - 1) / kPage + 2 + ((double)a.sinks + kPage - 1) / kPage;
+      pages = a.batch * std::min((double)a.max_blocks, std::floor(most)) * groups;
+    }
+    const double t = fixed[i] + page[i] * std::max(2.0, pages / (n == 128 ? sm_count / 2 : sm_count));
+    if (!tile || t < best) {
+      best = t;
+      tile = n;
+    }
+  }
+  return tile;
+}
+
+}  // namespace
+
+size_t plan_tile(TileArgs* a, int sm_count, int forced_workers, void* base) {
+  return lay_out(a, pick_row_tile(*a, sm_count), sm_count, forced_workers, base);
+}
+
+size_t tile_bytes(TileArgs a, int sm_count, int forced_workers) {
+  const int forced = knob_value(MLA_KNOB_ROW_TILE);
+  const bool few = (a.prefix_len ? (long long)a.batch * a.rows : a.rows) <= 16;  // never better in a wider tile
+  size_t most = 0;
+  for (int n : kRowTiles)
+    if (n == 16 || n == forced || !few) most = std::max(most, lay_out(&a, n, sm_count, forced_workers, nullptr));
+  return most;
 }
 
 void tile_schedule(TileArgs* a) {
@@ -841,19 +919,15 @@ cudaError_t launch_decode_tile(const TileArgs& a, cudaStream_t stream) {
   const bool shared = a.prefix_len != nullptr;
   cudaError_t e;
   if (a.row_tile == 128) e = launch_decode_tile_pair(a, stream);
-  else if (shared)
-    e = a.row_tile == 16   ? launch_tile<16, true>(a, stream)
-        : a.row_tile == 32 ? launch_tile<32, true>(a, stream)
-                           : launch_tile<64, true>(a, stream);
-  else
-    e = a.row_tile == 16   ? launch_tile<16, false>(a, stream)
-        : a.row_tile == 32 ? launch_tile<32, false>(a, stream)
-                           : launch_tile<64, false>(a, stream);
+  else if (shared) e = a.row_tile == 16 ? launch_tile<16, true>(a, stream) : launch_tile<32, true>(a, stream);
+  else e = a.row_tile == 16 ? launch_tile<16, false>(a, stream) : launch_tile<32, false>(a, stream);
   if (e != cudaSuccess) return e;
   // As many CTAs as run at once; each takes rows until they are done.
-  const int grid = std::min((a.batch * a.rows + kCombineRows - 1) / kCombineRows, a.sm_count * kCombineCtas);
-  return shared ? launch_dependent(combine_tile_kernel<true>, grid, kCombineThreads, 0, stream, a)
-                : launch_dependent(combine_tile_kernel<false>, grid, kCombineThreads, 0, stream, a);
+  const int R = a.batch * a.rows;
+  if (R <= 2 * a.sm_count)
+    return shared ? launch_combine_tile<true, 4>(a, R, stream) : launch_combine_tile<false, 4>(a, R, stream);
+  const int grid = std::min((R + 3) / 4, 3 * a.sm_count);
+  return shared ? launch_combine_tile<true, 1>(a, grid, stream) : launch_combine_tile<false, 1>(a, grid, stream);
 }
 
 }  // namespace mla

@@ -4,12 +4,14 @@
 //     S[128 x 128]  = q'[128 x 576] . K^T   CTA r supplies page r of the step, all dims
 //     O[128 x 512] += P[128 x 128] . V      two MMAs of N = 256 dims; CTA r supplies dims
 //                                           [256r + 128j, +128) of both pages for MMA j
-// A 64-row tile on one CTA (decode_tile.cu) is bound by shared-memory bandwidth: its M = 64
-// products read 4 KB for 32 cycles and 6 KB for 48 cycles of tensor work (measured: 32.2 and
-// 48.2 cycles a MMA, 128 bytes a cycle), ~3,500 cycles per 64 rows x 64 tokens with the loads
-// on top.  The pair's products take 1,088 cycles for the same work, read 2 KB (4 KB
-// where q' is in shared memory) per 32 cycles and 6 KB per 64, and a page's rows serve twice
-// as many queries.  Each CTA keeps the scores and outputs of its own rows, so the softmax
+// A tile of 64 rows on one CTA was bound by shared-memory bandwidth: its M = 64 products read
+// 4 KB for 32 cycles and 6 KB for 48 cycles of tensor work (32.2 and 48.2 cycles a MMA, 128
+// bytes a cycle), ~3,500 cycles per 64 rows x 64 tokens with the loads on top.  The pair's
+// products take 1,088 cycles for the same work (32.2 and 64.2 cycles a MMA), read 2 KB (4 KB
+// where q' is in shared memory) per 32 cycles and 5 KB per 64 (P is taken from the collector
+// the second time), and a page's rows serve twice as many queries: a step takes 2,400 to 2,800
+// cycles of 2,176 of tensor work (at the 1.5 to 1.8 GHz that the power limit leaves under this
+// load; 1.4 to 1.6 us).  Each CTA keeps the scores and outputs of its own rows, so the softmax
 // needs nothing from the peer.  The value half that a CTA supplies is loaded apart from its
 // score page (1.8 times the page's bytes, the second time from L2).
 //

@@ -104,7 +104,7 @@ int decode_pair_max_workers(int sm_count);
 cudaError_t launch_decode(int kernel, const DecodeArgs& a, cudaStream_t stream);
 int decode_granule(int kernel);
 
-// Sliding-window and shared-prefix decode: query rows in tiles of row_tile (16, 32 or 64
+// Sliding-window and shared-prefix decode: query rows in tiles of row_tile (16 or 32
 // with one CTA per worker, decode_tile.cu, or 128 with a CTA pair, decode_tile_pair.cu).  The schedule's entries ("tasks") are,
 // for a window, the sequences (worker w of group g walks the pages for rows [g row_tile, +)
 // of each sequence, so the `groups` CTAs or pairs of one worker read the same pages side by
@@ -135,9 +135,10 @@ struct TileArgs {
 };
 
 // Fills row_tile, groups, tiles, num_workers and the workspace pointers for the sizes
-// already in `a`; returns the workspace bytes (`base` may be null to compute the size).
-// forced_workers > 0 sets the number of workers.
+// already in `a`; returns the workspace bytes.  forced_workers > 0 sets the number of workers.
 size_t plan_tile(TileArgs* a, int sm_count, int forced_workers, void* base);
+// The most workspace that any row tile needs for a's batch, rows and kind.
+size_t tile_bytes(TileArgs a, int sm_count, int forced_workers);
 // Sets the schedule's constants for the current knobs.
 void tile_schedule(TileArgs* a);
 cudaError_t launch_decode_tile(const TileArgs& a, cudaStream_t stream);

@@ -53,6 +53,8 @@ __device__ __forceinline__ int prefix_pages(const TileArgs& a) { return seq_page
 __device__ __forceinline__ int tile_seq0(const TileArgs& a, int t) { return t * a.row_tile / a.rows; }
 __device__ __forceinline__ int tile_seq1(const TileArgs& a, int t) { return (min((t + 1) * a.row_tile, a.batch * a.rows) - 1) / a.rows; }
 
+static __device__ __noinline__ int tile_pages(const TileArgs& a, int t);
+
 template <bool kShared>
 struct TaskLengths {
   const TileArgs* a;
@@ -67,6 +69,19 @@ struct TaskLengths {
 #pragma unroll 8
     for (int b = tile_seq0(*a, t); b <= b1; ++b) n += own_pages(*a, b);
     return n;
+  }
+  // pages(thread) for thread < tasks, else 0, by whole warps: a few tiles of many sequences
+  // (one of 128 took 11 us by one thread) are counted by a warp each.
+  __device__ __forceinline__ int mine(int thread, int tasks) const {
+    if (kShared && a->row_tile > 8 * a->rows * tasks) {
+      int n = 0;
+      for (int j = 0; j < 32 && (thread & ~31) + j < tasks; ++j) {
+        const int v = tile_pages(*a, (thread & ~31) + j);
+        if ((thread & 31) == j) n = v;
+      }
+      return n;
+    }
+    return thread < tasks ? pages(thread) : 0;
   }
 };
 

@@ -42,6 +42,8 @@ struct SeqLengths {
   const int32_t* seqlens;
   int max_blocks;
   __device__ __forceinline__ int pages(int b) const { return seq_pages(seqlens, max_blocks, b); }
+  // pages(thread) for thread < B, else 0 (called by every thread of the CTA).
+  __device__ __forceinline__ int mine(int thread, int B) const { return thread < B ? pages(thread) : 0; }
   __device__ __forceinline__ bool bad(int b) const {
     const int T = seqlens[b];
     return T < 0 || T > max_blocks * kPage;
@@ -103,7 +105,7 @@ static __device__ __noinline__ void derive_range(const Lengths len, int B, int P
   // 0. As many threads as sequences: one read of the lengths, one exchange between warps
   // (2.0 -> 1.1 us at one sequence and 256, most of it the read).
   if (B <= (int)blockDim.x) {
-    const int n = tid < B ? len.pages(tid) : 0;
+    const int n = len.mine(tid, B);
     const bool bad = tid < B && len.bad(tid);
     const int u = units(n);
     int x = u;

@@ -19,11 +19,12 @@ from gpu_helpers import bf16_dev
 
 pytestmark = pytest.mark.gpu
 
-KNOBS = ("num_workers", "min_pages", "split_policy", "piece_cost", "wait_limit", "withhold_arrive")
+KNOBS = ("num_workers", "min_pages", "split_policy", "piece_cost", "wait_limit", "withhold_arrive", "row_tile")
 
 
-@pytest.fixture(autouse=True)
-def _knobs():
+@pytest.fixture(autouse=True, params=[0, 16, 32, 128], ids=["auto", "tile16", "tile32", "tile128"])
+def _knobs(request):
+    M.mla_set_knob("row_tile", request.param)
     yield
     for k in KNOBS:
         M.mla_set_knob(k, 0)
