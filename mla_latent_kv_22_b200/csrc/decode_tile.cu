@@ -902,11 +902,12 @@ void tile_schedule(TileArgs* a) {
   const int policy = knob_value(MLA_KNOB_SPLIT_POLICY);
   a->granule = a->row_tile == 128 ? 2 : 1;  // pages per step
   a->min_pages = mp > 0 ? mp : 2;
-  // A piece costs a pair as much as 10 of its pages, a single CTA as much as 3 (us at 4 / 7 /
-  // 10 / 13 pages: pair, 64 sequences of 128 heads sharing 8,192 tokens 161 / 137 / 146 / 154,
-  // 32 sharing 2,000 44 / 37 / 36 / 38; single, at 0 / 3 / 6 / 9, 16 heads of 128 sequences
-  // sharing 1,000 47 / 41 / 41 / 43, 32 heads over a window of 4,096 44 / 42 / 40 / 39).
-  a->piece_cost = pc > 0 ? std::min(pc - 1, kMaxPieceCost) : a->row_tile == 128 ? 10 : 3;
+  // A piece costs a pair as much as 10 of its pages, a single CTA, whose stores overlap, as much
+  // as one (us at 4 / 7 / 10 / 13 pages: pair, 64 sequences of 128 heads sharing 8,192 tokens
+  // 161 / 137 / 146 / 154, 32 sharing 2,000 44 / 37 / 36 / 38; single, at 0 / 1 / 2 / 3, 16
+  // heads over 256 windows of 1,021 67.3 / 67.2 / 68.3 / 69.2, over 200 of 4,096 143 / 142 /
+  // 148 / 152, 8 sequences of 8 heads behind 4,000 tokens 16.1 / 15.0 / 15.0 / 15.0).
+  a->piece_cost = pc > 0 ? std::min(pc - 1, kMaxPieceCost) : a->row_tile == 128 ? 10 : 1;
   // Sequences (or tiles) run whole when splitting them would save less than it costs: to a
   // pair, of R rows in all, 10 + R / 512 pages (a piece more per worker, fp32 partials and
   // their merge; whole / split us: 64 windows of 65 pages for 128 heads 75 / 86, of 1 to 34
