@@ -237,14 +237,16 @@ mla_status_t mla_append(const void* c_kv, const void* k_rope, const void* q_rope
  * lse     device fp32 [batch, s_q, heads], fully overwritten
  * A query that sees no token gets out = 0, lse = -inf.  Block-table entries of pages
  * wholly outside the sinks and every query's window are never read (such pages may have
- * been given back), and cached rows that no query of the sequence sees may hold anything;
- * a NaN or infinity in a row that some query of the sequence sees may reach the others.
+ * been given back), and what a query does not see never reaches it: cached rows outside
+ * its sight, other sequences and other queries may hold anything, NaN included.
  * s_q, heads, kv_cache, block_table, cache_seqlens, softmax_scale, errors: as in
  * mla_decode_multi.
  * workspace: device memory of at least mla_decode_window_workspace_size bytes, 256-byte
  * aligned, the caller's: calls that may overlap on the GPU (streams, captured graphs)
  * need one each.  It holds nothing between calls.  Results depend on (batch, s_q, heads,
- * window, sinks, cache_seqlens, the device's SM count), not on page ids or on what ran before.
+ * window, sinks, cache_seqlens, max_blocks, the device's SM count), not on page ids or on
+ * what ran before: the same call gives the same bits.  (max_blocks bounds the pages, from
+ * which the width of the query tiles is chosen: it may move a result by its rounding.)
  */
 size_t mla_decode_window_workspace_size(int batch, int s_q, int heads);
 mla_status_t mla_decode_window(const void* q, const void* kv_cache, const int32_t* block_table,
@@ -267,8 +269,9 @@ mla_status_t mla_decode_window(const void* q, const void* kv_cache, const int32_
  * block_table  device int32 [batch, max_blocks]: pages of each sequence's own tokens; the
  *              first of them starts a page, whatever P is
  * cache_seqlens device int32 [batch], the own tokens, 0 <= T_b <= max_blocks * 64
- * q, out, lse, s_q, heads, softmax_scale, workspace, empty queries, errors: as in
- * mla_decode_window (an invalid prefix_len makes every row NaN).
+ * q, out, lse, s_q, heads, softmax_scale, workspace, empty queries, errors, sight: as in
+ * mla_decode_window (prefix_blocks counts like max_blocks; an invalid prefix_len makes every
+ * row NaN, an invalid length or own page the rows of its sequence).
  */
 size_t mla_decode_shared_workspace_size(int batch, int s_q, int heads);
 mla_status_t mla_decode_shared(const void* q, const void* kv_cache, const int32_t* prefix_table, const int32_t* prefix_len,

@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint32_t tmem_base_s;
   __shared__ Ctl ctl_s;
   constexpr int kWords = (N + 31) / 32;
-  __shared__ uint32_t bad_s[8][kWords];  // [piece % 8] a bit for each row that a page id outside the cache spoils
+  __shared__ uint32_t bad_s[16][kWords];  // [piece % 16] a bit for each row that a page id outside the cache spoils
   __shared__ RangeScratch range_s;
   // Rescale factors and whether a warp has any.  Four pages deep: a warp may be three pages
   // ahead of another across the end of a piece, where they do not meet.
@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     ctl_s = Ctl{a.err, limit_ns, 0};
-    for (int i = 0; i < 8 * kWords; ++i) bad_s[i / kWords][i % kWords] = 0;
+    for (int i = 0; i < 16 * kWords; ++i) bad_s[i / kWords][i % kWords] = 0;
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(bar(kFull + s), 1);   // the producer, or the cleaning warp
       mbar_init(bar(kEmpty + s), 1);  // MMA commit
@@ -308,13 +308,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     int withheld = -1;
     bool ok = true;
     while (ok && ld.next()) {
-      // The marks four pieces on are those of four pieces back: read, since these loads run
-      // less than four pieces ahead of the softmax (at most five halves of pages).
-      if (lane < kWords) bad_s[(piece + 4) & 7][lane] = 0;
+      // The marks eight pieces on are those of eight pieces back, long read: five ring slots
+      // hold halves of at most three pieces whose second product is not done.
+      if (lane < kWords) bad_s[(piece + 8) & 15][lane] = 0;
       __syncwarp();
       for (int p = ld.pc.pa; p < ld.pc.pe && ok; ++p, ++g) {
         bool dirty;
-        const int y = ld.row(p, dirty, bad_s[piece & 7]);
+        const int y = ld.row(p, dirty, bad_s[piece & 15]);
 #pragma unroll 1
         for (int m = 0; m < 2; ++m) {
           // The page's rope rides on its second half, whose ring slot was last held by the
@@ -649,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       // ---- the piece's row factors for the storing warps, and lse
       const bool bad =
-          sight.bad || (holds && ((const_cast<volatile uint32_t&>(bad_s[piece & 7][row >> 5]) >> (row & 31)) & 1u));
+          sight.bad || (holds && ((const_cast<volatile uint32_t&>(bad_s[piece & 15][row >> 5]) >> (row & 31)) & 1u));
       const float l_row = l + __shfl_xor_sync(0xffffffffu, l, 16);
       const bool none = l_row == 0.f;  // the row sees no token of the piece
       if (piece >= kOBufs && !wait_all(bar(kOFree + ob), (piece / kOBufs - 1) & 1, ctl)) break;

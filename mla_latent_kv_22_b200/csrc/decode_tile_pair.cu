@@ -228,7 +228,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __shared__ __align__(8) uint64_t bars[kNumBars];
   __shared__ uint32_t tmem_base_s;
   __shared__ Ctl ctl_s;
-  __shared__ uint32_t bad_s[8][4];  // [piece % 8] a bit for each row that a page id outside the cache spoils
+  __shared__ uint32_t bad_s[16][4];  // [piece % 16] a bit for each row that a page id outside the cache spoils
   __shared__ RangeScratch range_s;
   __shared__ uint32_t drop_s[4][4];  // CTA 0: [step % 4][32 tokens] to be looked at (nonfinite_seen)
   __shared__ float mx_s[2][2][2][64];  // [step parity][page][column half][row]
@@ -246,7 +246,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     ctl_s = Ctl{a.err, limit_ns, 0, map_to_rank(smem_u32(&ctl_s.abort), rank ^ 1u)};
-    for (int i = 0; i < 32; ++i) bad_s[i / 4][i % 4] = 0;
+    for (int i = 0; i < 64; ++i) bad_s[i / 4][i % 4] = 0;
     for (int i = 0; i < 16; ++i) drop_s[i / 4][i % 4] = 0;
     for (int s = 0; s < kKSlots; ++s) {
       mbar_init(bar(kFullK + s), 1);   // CTA 0's producer arms it with both CTAs' bytes
@@ -366,15 +366,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t full0 = bar0(kFullV);
     while (ok && ld.next()) {
       const int steps = (ld.pc.pe - ld.pc.pa + 1) / 2;
-      // The marks four pieces on are those of four pieces back: read, since these loads run
-      // less than three pieces ahead of the softmax.
-      if (lane < 4) bad_s[(piece + 4) & 7][lane] = 0;
+      // The marks eight pieces on are those of eight pieces back, long read: these loads are
+      // at most a step ahead of the value MMAs.
+      if (lane < 4) bad_s[(piece + 8) & 15][lane] = 0;
       __syncwarp();
       for (int i = 0; i < steps && ok; ++i, ++g) {
         bool dirty[2];
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
-          const int y = ld.row(ld.pc.pa + 2 * i + m, dirty[m], bad_s[piece & 7]);
+          const int y = ld.row(ld.pc.pa + 2 * i + m, dirty[m], bad_s[piece & 15]);
           if (!wait_all(bar(kEmptyV + m), (g & 1) ^ 1, ctl)) { ok = false; break; }
           if (lane == 0) {
             const uint32_t dst = sbase + kOffV + m * kSlotBytes;
@@ -717,7 +717,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const float l_row = (lsum_s[0][0][h] + lsum_s[0][1][h]) + (lsum_s[1][0][h] + lsum_s[1][1][h]);
       if (!wait_all(bar(kODone), ge & 1, ctl)) { ok = false; break; }
       tc_fence_after();
-      const bool bad = k.sight.bad || ((const_cast<volatile uint32_t&>(bad_s[piece & 7][row >> 5]) >> (row & 31)) & 1u);
+      const bool bad = k.sight.bad || ((const_cast<volatile uint32_t&>(bad_s[piece & 15][row >> 5]) >> (row & 31)) & 1u);
       const bool none = l_row == 0.f;  // the row sees no token of the piece
       const float inv = bad ? NAN : (none ? 0.f : 1.f / l_row);
       const PieceOut to = piece_out<kRows, kShared>(a, k.t, pc, pi.rg, w, grp);
