@@ -45,6 +45,19 @@ def test_shared_pieces_cut_anywhere(workers):
     assert_rounded(out, lse, c.ref())
 
 
+# Pieces of one step in front: the next one's loads find free slots before its turn.
+@pytest.mark.parametrize("workers", [1, 3])
+@pytest.mark.parametrize("lens", [[1] * 12, [128, 64, 1, 129, 300, 90], [257, 1, 700, 2, 2, 640], [0, 100, 0, 64, 500]])
+def test_first_pieces_of_one_step(lens, workers):
+    M.mla_set_knob("num_workers", workers)
+    c, q = window_case(lens, 1, 128, 1024, 0, seed=760 + len(lens))
+    want = ref(c, q, 1024, 0)
+    for _ in range(20):
+        out, lse, err = run(c, q, 1024, 0)
+        assert err == 0
+    assert_rounded(out, lse, want)
+
+
 @pytest.mark.parametrize("shared", [False, True])
 def test_growing_scores_rescale_a_pair(shared):
     # The rope dims grow along the tokens, so the reference maximum moves many times.
