@@ -10,6 +10,7 @@ no fallback.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 
 import torch
@@ -350,7 +351,7 @@ def mla_decode_window(q, kv_cache, block_table, cache_seqlens, out, lse, softmax
     q [B,H,576] or [B,s_q,H,576] bf16; out like q with 512, bf16; lse fp32; the cache
     arguments are those of mla_decode.  ``workspace``: a CUDA uint8 tensor of at least
     mla_decode_window_workspace_size(B, s_q, H) bytes, or None to take one from torch's
-    allocator for this call."""
+    allocator for this call.  ``window`` and ``sinks`` may be larger than any sequence."""
     if workspace is None and stream is None and _quick(_binding.decode_window(
             q, kv_cache, block_table, cache_seqlens, out, lse, softmax_scale, window, sinks)):
         return
@@ -361,6 +362,7 @@ def mla_decode_window(q, kv_cache, block_table, cache_seqlens, out, lse, softmax
     p_o = _here(out, "out", torch.bfloat16, rows + (D_LATENT,), dev)
     p_l = _here(lse, "lse", torch.float32, rows, dev)
     kv, max_blocks, num_pages, bt = _cache_here(kv_cache, block_table, B, dev)
+    window, sinks = (max(-1, min(operator.index(n), 2**31 - 1)) for n in (window, sinks))  # as 32-bit integers
     ws = _workspace(workspace, lib.mla_decode_window_workspace_size(B, SQ, H), stream, q.device, dev)
     _check(lib.mla_decode_window(p_q, kv, bt, lens, p_o, p_l, B, SQ, H, num_pages, max_blocks, window, sinks, softmax_scale,
                                  ws.data_ptr(), ws.numel(), _stream(stream, dev)))

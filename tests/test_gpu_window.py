@@ -161,6 +161,12 @@ def test_a_window_beyond_the_sequence_is_the_causal_decode():
     out, lse, err = run(c, q, (1 << 31) - 1, 0)
     assert err == 0
     assert_rounded(out, lse, ref(c, q, 10 ** 9, 0))
+    for big in (2 ** 32 + 1, 2 ** 63 - 1, np.int64(2 ** 40)):  # integers of more than 32 bits
+        o2, l2, err = run(c, q, big, 0)
+        assert err == 0 and torch.equal(o2, out) and torch.equal(l2, lse)
+    for bad in (-2 ** 32 + 5, -2 ** 40):
+        with pytest.raises(M.MlaError):
+            run(c, q, bad, 0)
 
 
 @pytest.mark.parametrize("H", [16, 128])
