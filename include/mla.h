@@ -209,7 +209,8 @@ mla_status_t mla_decode_noalloc(const void* q, const void* kv_cache, const int32
  * pos_offset device int32 [batch], or NULL for 0 (e.g. the length of a shared prefix whose
  *            pages are not in block_table)
  * block_table, kv_cache, cache_seqlens: as in mla_decode (block_table NULL = contiguous)
- * Strides are elements, multiples of 8; vectors are dense.  A token whose length, row or
+ * Strides are elements, multiples of 8 (that of a single token or head may be anything);
+ * vectors are dense.  A token whose length, row or
  * page id is invalid sets MLA_ERR_DEVICE_BAD_PAGE, one whose position is outside
  * [0, max_pos) MLA_ERR_DEVICE_BAD_POSITION: no cache row is written for it and its q_out
  * is NaN.  Two tokens given the same cache row race.

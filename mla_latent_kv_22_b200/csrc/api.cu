@@ -624,7 +624,10 @@ mla_status_t mla_append(const void* c_kv, const void* k_rope, const void* q_rope
   if ((reinterpret_cast<uintptr_t>(cu_tokens) | reinterpret_cast<uintptr_t>(cache_seqlens) |
        reinterpret_cast<uintptr_t>(pos_offset) | reinterpret_cast<uintptr_t>(block_table)) & 3u)
     return fail(MLA_ERR_INVALID_ARG, "int32 arrays must be 4-byte aligned");
-  int64_t strides[6] = {c_kv_stride, k_rope_stride, q_stride_token, q_stride_head, q_out_stride_token, q_out_stride_head};
+  // The stride of a single token or head is never used, and may be anything.
+  if (tokens == 1) c_kv_stride = k_rope_stride = q_stride_token = q_out_stride_token = 0;
+  if (heads == 1) q_stride_head = q_out_stride_head = 0;
+  const int64_t strides[6] = {c_kv_stride, k_rope_stride, q_stride_token, q_stride_head, q_out_stride_token, q_out_stride_head};
   for (int i = 0; i < (q_rope ? 6 : 2); ++i)
     if (strides[i] % 8) return fail(MLA_ERR_INVALID_ARG, "strides must be multiples of 8 elements (16 bytes)");
 

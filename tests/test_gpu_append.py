@@ -133,6 +133,17 @@ def test_views_and_rotation_in_place(inter):
     assert (q[..., :128] == 0).all()
 
 
+def test_a_single_token_or_head_of_any_stride():
+    c = Append([1], [70], 1, seed=760)
+    d = c.dev()
+    odd = lambda t, *st: t.as_strided(t.shape, st)
+    d.update(c_kv=odd(d["c_kv"], 577, 1), k_rope=odd(d["k_rope"], 3, 1), q_rope=odd(d["q_rope"], 129, 67, 1),
+             q_out=odd(d["q_out"], 65, 65, 1))
+    M.mla_append(**d)
+    assert M.mla_get_device_error() == 0
+    c.check(d["kv_cache"], d["q_out"])
+
+
 def test_bad_tokens_write_nothing():
     c = Append([1, 2, 1, 1], [10, 70, 5, 6], 4, seed=722)
     c.table[1, 1] = c.kv.shape[0]            # sequence 1's new rows lie there
