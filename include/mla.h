@@ -245,9 +245,10 @@ mla_status_t mla_append(const void* c_kv, const void* k_rope, const void* q_rope
  * workspace: device memory of at least mla_decode_window_workspace_size bytes, 256-byte
  * aligned, the caller's: calls that may overlap on the GPU (streams, captured graphs)
  * need one each.  It holds nothing between calls.  Results depend on (batch, s_q, heads,
- * window, sinks, cache_seqlens, max_blocks, the device's SM count), not on page ids or on
- * what ran before: the same call gives the same bits.  (max_blocks bounds the pages, from
- * which the width of the query tiles is chosen: it may move a result by its rounding.)
+ * window, sinks, cache_seqlens, max_blocks, the device's SMs), not on page ids or on what
+ * ran before: the same call gives the same bits.  (max_blocks bounds the pages, from which
+ * the width of the query tiles and the split of short calls are chosen: it may move a
+ * result by its rounding.)
  */
 size_t mla_decode_window_workspace_size(int batch, int s_q, int heads);
 mla_status_t mla_decode_window(const void* q, const void* kv_cache, const int32_t* block_table,

@@ -1,5 +1,6 @@
 // Sliding-window and shared-prefix decode: split-KV absorbed decode with one CTA per
-// worker, a tile of N = 16 or 32 query rows and one 64-token page per step.
+// worker, a tile of N = 16 or 32 query rows and one 64-token page per step.  The pieces of
+// split tiles are merged by a second grid, in short calls by the cluster that made them.
 //
 // A page is loaded once and feeds both products from the same shared memory:
 //     S[64 x 64]    = q'[N x 576] . K^T       (M = 64 rows, N = 64 tokens, K = 576)
@@ -38,6 +39,8 @@
 // MLA_ERR_DEVICE_TIMEOUT, drains its work in flight and returns.  No trap.
 #include <cuda.h>
 #include <cudaTypedefs.h>
+
+#include <atomic>
 
 #include <algorithm>
 #include <cmath>
@@ -224,7 +227,155 @@ __device__ __noinline__ void drop_values(uint8_t* h0, uint8_t* h1, uint32_t word
   __syncwarp();
 }
 
+// ---------------------------------------------------------------- combine
+// Merges the pieces of a row's task by their lse, in the order of their pages, and writes the
+// rows that no piece holds.  Four warps take a row, 128 dims each, with four pieces' loads in
+// flight, the first four before the weights are known.  Where there are few rows, each of
+// kSplit = 4 such groups takes a quarter of the pieces, and the first adds them up in order
+// (a call of 30 rows in 148 pieces 30.4 -> 21.5 us).
+constexpr int kCombineThreads = 512;
+
+template <int kSplit>
+struct MergeScratch {
+  float4 acc[kSplit][128];
+  float wsum[kSplit][4];
+};
+
+// Row r of sequence b, row gr of the batch's, whose task's record is s.
+template <bool kShared, int kSplit, int kLoads>
+__device__ __forceinline__ void merge_row(const TileArgs& a, int gr, int b, int r, const SeqInfo s, int split,
+                                          MergeScratch<kSplit>* sm) {
+  const int lane = threadIdx.x & 31, part = (threadIdx.x >> 5) & 3, N = a.row_tile;
+  bool nan = s.num_pieces < 0;
+  if (kShared && bad_length(a.seqlens[b], a.max_blocks)) {
+    set_device_error(a.err, MLA_ERR_DEVICE_BAD_PAGE);
+    nan = true;
+  }
+  if (s.num_pieces == 1) return;  // written by the decode grid
+  const int n = max(s.num_pieces, 0);
+  // Storage row of piece k; a window's groups lie side by side, N rows each.
+  const size_t stride = kShared ? N : (size_t)a.groups * N;
+  const int r0 = kShared ? gr % N : r;
+  auto at = [&](int k) -> size_t { return (size_t)(k == 0 ? s.first_slot : s.first_worker + k) * stride + r0; };
+  // This group's pieces [ka, ke): whole rounds of loads.
+  const int per = kSplit > 1 ? ((n + kLoads * kSplit - 1) / (kLoads * kSplit)) * kLoads : n, ka = split * per, ke = min(n, ka + per);
+  float4 x[kLoads];
+  auto load = [&](int k0) {
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j)
+      x[j] = k0 + j < ke ? reinterpret_cast<const float4*>(a.part_o + at(k0 + j) * kDLatent)[32 * part + lane]
+                         : make_float4(0.f, 0.f, 0.f, 0.f);
+  };
+  load(ka);
+  float L = -INFINITY;
+#pragma unroll 1
+  for (int k = lane; k < n; k += 32) {
+    const float v = a.part_lse[at(k)];
+    nan |= v != v;
+    L = fmaxf(L, v);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) L = fmaxf(L, __shfl_xor_sync(0xffffffffu, L, o));
+  uint2* const out2 = reinterpret_cast<uint2*>(a.out + (size_t)gr * kDLatent) + 32 * part + lane;
+  nan = __any_sync(0xffffffffu, nan);
+  if (nan || L == -INFINITY) {  // alike in all groups of a row
+    const uint32_t v = nan ? 0x7fff7fffu : 0u;
+    if (split == 0) *out2 = make_uint2(v, v);
+    if (split == 0 && part == 0 && lane == 0) a.lse[gr] = nan ? NAN : -INFINITY;
+    return;
+  }
+  float acc[4] = {0.f, 0.f, 0.f, 0.f}, wsum = 0.f, mine = 0.f;
+#pragma unroll 1
+  for (int k0 = ka; k0 < ke; k0 += kLoads) {
+    if (k0 > ka) load(k0);
+    const int i = (k0 - ka) & 31;
+    if (i == 0) mine = k0 + lane < ke ? expf(a.part_lse[at(k0 + lane)] - L) : 0.f;  // the weights of 32 pieces
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      const float wk = __shfl_sync(0xffffffffu, mine, i + j);  // 0 past the last piece
+      wsum += wk;
+      acc[0] += wk * x[j].x;
+      acc[1] += wk * x[j].y;
+      acc[2] += wk * x[j].z;
+      acc[3] += wk * x[j].w;
+    }
+  }
+  if (kSplit > 1) {
+    sm->acc[split][32 * part + lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    if (lane == 0) sm->wsum[split][part] = wsum;
+    __syncthreads();
+    if (split == 0) {
+#pragma unroll
+      for (int g = 1; g < kSplit; ++g) {
+        const float4 y = sm->acc[g][32 * part + lane];
+        acc[0] += y.x;
+        acc[1] += y.y;
+        acc[2] += y.z;
+        acc[3] += y.w;
+        wsum += sm->wsum[g][part];
+      }
+    }
+    __syncthreads();
+  }
+  if (split == 0) {
+    const float inv = 1.f / wsum;
+    *out2 = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+    if (part == 0 && lane == 0) a.lse[gr] = L + logf(wsum);
+  }
+}
+
+template <bool kShared, int kSplit>
+__global__ void __launch_bounds__(kCombineThreads, 3) combine_tile_kernel(const __grid_constant__ TileArgs a) {
+  constexpr int kRows = kCombineThreads / (128 * kSplit);  // rows at a time
+  __shared__ MergeScratch<kSplit> scratch;
+  grid_dep_launch_dependents();
+  grid_dep_wait();
+  const int group = threadIdx.x >> 7, R = a.batch * a.rows;
+#pragma unroll 1
+  for (int gr = blockIdx.x * kRows + (kSplit > 1 ? 0 : group); gr < R; gr += gridDim.x * kRows) {
+    const int b = gr / a.rows;
+    merge_row<kShared, kSplit, 4>(a, gr, b, gr - b * a.rows, a.task[kShared ? gr / a.row_tile : b], kSplit > 1 ? group : 0, &scratch);
+  }
+}
+
+// ---------------------------------------------------------------- teams
+// A short call: a cluster of 8 or 16 CTAs (the team) per row tile shares out the tile's pages
+// evenly and merges its pieces itself, behind a barrier of the cluster instead of in a second
+// grid.  Such a call is a chain of latencies (lengths, table, page, the two products, store,
+// merge); the team takes the second grid's start and the exchange over the batch's lengths
+// out of it, and its launch off the host (9.7 -> 5.9 us a call).  us, split schedule / team of 8 / of 16: 16 heads over a window of 512 10.6 /
+// 10.9 / 10.0, of 64 11.8 / 9.4 / 9.5; 2 such windows of 512 11.5 / 11.1 / 10.0, 14 of them
+// 13.4 / 11.9 / -; 7 sequences of 16 heads behind 1,000 tokens 14.0 / 13.7 / 13.4.
+
+// The team's record of tile (t, grp), and this CTA's range of its pages.
+template <bool kShared>
+static __device__ __noinline__ void team_range(const TileArgs& a, int t, int rank, volatile WorkerRange& rg, SeqInfo& s) {
+  const TaskLengths<kShared> len{&a};
+  const bool bad = len.bad(t);
+  const int n = task_pages<kShared>(a, t), q = max((n + a.team - 1) / a.team, a.min_pages), pa = rank * q, pe = min(pa + q, n);
+  if (threadIdx.x == 0) {
+    if (bad && rank == 0) set_device_error(a.err, MLA_ERR_DEVICE_BAD_PAGE);
+    const int b = pa < pe ? t : -1;
+    rg.b0 = rg.b1 = b;
+    rg.p0 = pa;
+    rg.p1 = pe;
+    s = SeqInfo{a.team * t, bad ? -1 : (n + q - 1) / q, a.team * t};
+  }
+  __syncthreads();
+}
+
+// The team's rows, eight CTAs by three groups of 128 threads at a time.
 template <int N, bool kShared>
+static __device__ __noinline__ void team_merge(const TileArgs& a, int t, int grp, int rank, const SeqInfo& s) {
+  const Task k = load_task<N, kShared>(a, t, grp);
+#pragma unroll 1
+  for (int row = rank + a.team * (threadIdx.x >> 7); row < k.live; row += a.team * (kThreads / 128)) {
+    const int gr = k.row0 + row, b = gr / a.rows;
+    merge_row<kShared, 1, 8>(a, gr, b, gr - b * a.rows, s, 0, static_cast<MergeScratch<1>*>(nullptr));
+  }
+}
+
+template <int N, bool kShared, bool kTeam>
 __global__ void __launch_bounds__(kThreads, 1)
     decode_tile_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap rope_map,
                        const __grid_constant__ CUtensorMap q_map,
@@ -240,6 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kWords = (N + 31) / 32;
   __shared__ uint32_t bad_s[16][kWords];  // [piece % 16] a bit for each row that a page id outside the cache spoils
   __shared__ RangeScratch range_s;
+  __shared__ SeqInfo team_s;
   // Rescale factors and whether a warp has any.  Four pages deep: a warp may be three pages
   // ahead of another across the end of a piece, where they do not meet.
   constexpr int kAhead = 2 * Lay::kPBufs;
@@ -251,8 +403,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sbase = smem_u32(smem);
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int w = kShared ? blockIdx.x : blockIdx.x / a.groups;
-  const int grp = kShared ? 0 : blockIdx.x % a.groups;
+  const int unit = kTeam ? blockIdx.x / a.team : blockIdx.x, rank = kTeam ? blockIdx.x % a.team : 0;
+  const int w = (kShared ? unit : unit / a.groups) * (kTeam ? a.team : 1) + rank;
+  const int grp = kShared ? 0 : unit % a.groups;
   const int np = a.block_table ? a.num_pages : a.batch * a.max_blocks;
 
   if (tid == 0) {
@@ -292,8 +445,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Everything above overlaps the previous grid on the stream; from here on its writes
   // (the lengths, q', the tables, the cache) are visible.
   grid_dep_wait();
-  derive_range(TaskLengths<kShared>{&a}, kShared ? a.tiles : a.batch, a.num_workers, a.min_pages,
-               a.granule, a.whole_slack, a.piece_cost, a.task, a.err, w, range_s);
+  if constexpr (kTeam)
+    team_range<kShared>(a, w / a.team, rank, range_s.rg, team_s);
+  else
+    derive_range(TaskLengths<kShared>{&a}, kShared ? a.tiles : a.batch, a.num_workers, a.min_pages,
+                 a.granule, a.whole_slack, a.piece_cost, a.task, a.err, w, range_s);
   const uint32_t tmem = tmem_base_s;
   Ctl* const ctl = &ctl_s;
 
@@ -697,124 +853,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
-}
-
-// ---------------------------------------------------------------- combine
-// Merges the pieces of a row's task by their lse, in the order of their pages, and writes the
-// rows that no piece holds.  Four warps take a row, 128 dims each, with four pieces' loads in
-// flight, the first four before the weights are known.  Where there are few rows, each of
-// kSplit = 4 such groups takes a quarter of the pieces, and the first adds them up in order
-// (a call of 30 rows in 148 pieces 30.4 -> 21.5 us).
-constexpr int kCombineThreads = 512;
-
-template <bool kShared, int kSplit>
-__global__ void __launch_bounds__(kCombineThreads, 3) combine_tile_kernel(const __grid_constant__ TileArgs a) {
-  constexpr int kRows = kCombineThreads / (128 * kSplit);  // rows at a time
-  __shared__ float4 acc_s[kSplit][128];
-  __shared__ float wsum_s[kSplit][4];
-  grid_dep_launch_dependents();
-  grid_dep_wait();
-  const int lane = threadIdx.x & 31, part = (threadIdx.x >> 5) & 3, group = threadIdx.x >> 7;
-  const int split = kSplit > 1 ? group : 0;
-  const int R = a.batch * a.rows, N = a.row_tile;
-#pragma unroll 1
-  for (int gr = blockIdx.x * kRows + (kSplit > 1 ? 0 : group); gr < R; gr += gridDim.x * kRows) {
-    const int b = gr / a.rows, r = gr - b * a.rows;
-    const SeqInfo s = a.task[kShared ? gr / N : b];
-    bool nan = s.num_pieces < 0;
-    if (kShared && bad_length(a.seqlens[b], a.max_blocks)) {
-      set_device_error(a.err, MLA_ERR_DEVICE_BAD_PAGE);
-      nan = true;
-    }
-    if (s.num_pieces == 1) continue;  // written by the decode grid
-    const int n = max(s.num_pieces, 0);
-    // Storage row of piece k; a window's groups lie side by side, N rows each.
-    const size_t stride = kShared ? N : (size_t)a.groups * N;
-    const int r0 = kShared ? gr % N : r;
-    auto at = [&](int k) -> size_t { return (size_t)(k == 0 ? s.first_slot : s.first_worker + k) * stride + r0; };
-    // This group's pieces [ka, ke): whole fours.
-    const int per = kSplit > 1 ? ((n + 4 * kSplit - 1) / (4 * kSplit)) * 4 : n, ka = split * per, ke = min(n, ka + per);
-    float4 x[4];
-    auto load = [&](int k0) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        x[j] = k0 + j < ke ? reinterpret_cast<const float4*>(a.part_o + at(k0 + j) * kDLatent)[32 * part + lane]
-                           : make_float4(0.f, 0.f, 0.f, 0.f);
-    };
-    load(ka);
-    float L = -INFINITY;
-#pragma unroll 1
-    for (int k = lane; k < n; k += 32) {
-      const float v = a.part_lse[at(k)];
-      nan |= v != v;
-      L = fmaxf(L, v);
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) L = fmaxf(L, __shfl_xor_sync(0xffffffffu, L, o));
-    uint2* const out2 = reinterpret_cast<uint2*>(a.out + (size_t)gr * kDLatent) + 32 * part + lane;
-    nan = __any_sync(0xffffffffu, nan);
-    if (nan || L == -INFINITY) {  // alike in all groups of a row
-      const uint32_t v = nan ? 0x7fff7fffu : 0u;
-      if (split == 0) *out2 = make_uint2(v, v);
-      if (split == 0 && part == 0 && lane == 0) a.lse[gr] = nan ? NAN : -INFINITY;
-      continue;
-    }
-    float acc[4] = {0.f, 0.f, 0.f, 0.f}, wsum = 0.f, mine = 0.f;
-#pragma unroll 1
-    for (int k0 = ka; k0 < ke; k0 += 4) {
-      if (k0 > ka) load(k0);
-      const int i = (k0 - ka) & 31;
-      if (i == 0) mine = k0 + lane < ke ? expf(a.part_lse[at(k0 + lane)] - L) : 0.f;  // the weights of 32 pieces
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float wk = __shfl_sync(0xffffffffu, mine, i + j);  // 0 past the last piece
-        wsum += wk;
-        acc[0] += wk * x[j].x;
-        acc[1] += wk * x[j].y;
-        acc[2] += wk * x[j].z;
-        acc[3] += wk * x[j].w;
-      }
-    }
-    if (kSplit > 1) {
-      acc_s[split][32 * part + lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-      if (lane == 0) wsum_s[split][part] = wsum;
-      __syncthreads();
-      if (split == 0) {
-#pragma unroll
-        for (int g = 1; g < kSplit; ++g) {
-          const float4 y = acc_s[g][32 * part + lane];
-          acc[0] += y.x;
-          acc[1] += y.y;
-          acc[2] += y.z;
-          acc[3] += y.w;
-          wsum += wsum_s[g][part];
-        }
-      }
-      __syncthreads();
-    }
-    if (split == 0) {
-      const float inv = 1.f / wsum;
-      *out2 = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
-      if (part == 0 && lane == 0) a.lse[gr] = L + logf(wsum);
-    }
+  if constexpr (kTeam) {
+    __syncwarp();
+    cluster_sync();  // the team's partials are written
+    team_merge<N, kShared>(a, w / a.team, grp, rank, team_s);
   }
 }
 
 template <bool kShared, int kSplit>
 cudaError_t launch_combine_tile(const TileArgs& a, int grid, cudaStream_t stream) {
-  return launch_dependent(combine_tile_kernel<kShared, kSplit>, grid, kCombineThreads, 0, stream, a);
+  return launch_dependent(combine_tile_kernel<kShared, kSplit>, grid, kCombineThreads, 0, 0, stream, a);
 }
 
-template <int N, bool kShared>
+template <int N, bool kShared, bool kTeam>
 cudaError_t launch_tile(const TileArgs& a, cudaStream_t stream) {
   static bool done[64] = {};
-  cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void*>(decode_tile_kernel<N, kShared>), Layout<N>::kAlloc, done);
+  cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void*>(decode_tile_kernel<N, kShared, kTeam>), Layout<N>::kAlloc, done);
   if (e != cudaSuccess) return e;
   CUtensorMap kv_map, rope_map, q_map;
   if (!tile_maps(a, N, 9, &kv_map, &rope_map, &q_map)) return cudaErrorInvalidValue;
   const uint64_t limit_ns = (uint64_t)a.wait_limit * 1000000ull;
-  return launch_dependent(decode_tile_kernel<N, kShared>, kShared ? a.num_workers : a.num_workers * a.groups, kThreads,
-                          Layout<N>::kAlloc, stream, kv_map, rope_map, q_map, a, limit_ns);
+  return launch_dependent(decode_tile_kernel<N, kShared, kTeam>, kShared ? a.num_workers : a.num_workers * a.groups, kThreads,
+                          Layout<N>::kAlloc, a.team, stream, kv_map, rope_map, q_map, a, limit_ns);
+}
+
+template <int N, bool kShared>
+cudaError_t launch_tile(const TileArgs& a, cudaStream_t stream) {
+  return a.team ? launch_tile<N, kShared, true>(a, stream) : launch_tile<N, kShared, false>(a, stream);
 }
 
 }  // namespace
@@ -822,6 +887,67 @@ cudaError_t launch_tile(const TileArgs& a, cudaStream_t stream) {
 namespace {
 
 constexpr int kRowTiles[] = {16, 32, 128};
+
+// How many teams of `size` CTAs run at once on the current device (a cluster's CTAs share a GPC,
+// and GPCs differ in size: 15 of 8 and 7 of 16 where this was measured).
+int teams_at_once(int size) {
+  static std::atomic<int> known[64][2];  // + 1
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  const auto allow_wide = [](auto fn) {  // clusters above the portable 8
+    return cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+  };
+  std::atomic<int>& k = known[dev][size > 8];
+  if (k.load() == 0) {
+    const auto kernel = decode_tile_kernel<16, false, true>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(size, 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = Layout<16>::kAlloc;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = size;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<16>::kAlloc) != cudaSuccess ||
+        !allow_wide(kernel) || !allow_wide(decode_tile_kernel<16, true, true>) || !allow_wide(decode_tile_kernel<32, false, true>) ||
+        !allow_wide(decode_tile_kernel<32, true, true>) ||
+        cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+      n = 0;
+      cudaGetLastError();  // no teams, then
+    }
+    k.store(n + 1);
+  }
+  return k.load() - 1;
+}
+
+// The most pages of a tile of n rows that the window or the tables allow.
+long long most_pages(const TileArgs& a, int n) {
+  if (a.prefix_len) {
+    const int seqs = a.rows % n == 0 ? 1 : n % a.rows == 0 ? n / a.rows : (n - 1) / a.rows + 2;
+    return a.prefix_blocks + (long long)a.max_blocks * std::min(seqs, a.batch);
+  }
+  const long long w = ((long long)a.window + a.s_q - 1) / kPage + 2 + ((long long)a.sinks + kPage - 1) / kPage;
+  return std::min<long long>(a.max_blocks, w);
+}
+
+// CTAs per team for tiles of n rows, or 0: teams that run at once, with so few pages each that
+// they end before the split schedule would, which has all SMs but two grids (a call of one
+// tile: 1 page, of up to 6: 2, of more: 3; us split / team: a window of 960 for 16 heads 11.2 /
+// 11.3 at 2 pages each, two of them 11.9 / 11.4; 7 sequences behind 2,000 tokens 15.4 / 14.8 at
+// 3, 3 of them 13.8 / 14.2).  A schedule knob means the split schedule.
+int team_size(const TileArgs& a, int n) {
+  if (n > 32 || knob_value(MLA_KNOB_NUM_WORKERS) || knob_value(MLA_KNOB_MIN_PAGES) || knob_value(MLA_KNOB_SPLIT_POLICY) ||
+      knob_value(MLA_KNOB_PIECE_COST))
+    return 0;
+  const long long tiles = a.prefix_len ? ((long long)a.batch * a.rows + n - 1) / n : (long long)a.batch * ((a.rows + n - 1) / n);
+  const long long pages = most_pages(a, n), most = tiles == 1 ? 1 : tiles <= 6 ? 2 : 3;
+  for (int size : {16, 8})
+    if (pages <= size * most && tiles * size <= a.sm_count && tiles <= teams_at_once(size)) return size;
+  return 0;
+}
 
 // The sizes that follow from a row tile, and the workspace (see plan_tile).
 size_t lay_out(TileArgs* a, int row_tile, int sm_count, int forced_workers, void* base) {
@@ -844,6 +970,8 @@ size_t lay_out(TileArgs* a, int row_tile, int sm_count, int forced_workers, void
   a->task = reinterpret_cast<SeqInfo*>(take(tasks * sizeof(SeqInfo)));
   a->part_lse = reinterpret_cast<float*>(take(rows * sizeof(float)));
   a->part_o = reinterpret_cast<float*>(take(rows * kDLatent * sizeof(float)));
+  a->team = base ? team_size(*a, row_tile) : 0;  // no more partials than of the split schedule's workers
+  if (a->team) a->num_workers = a->team * (shared ? a->tiles : a->batch);
   return off;
 }
 
@@ -870,8 +998,7 @@ int pick_row_tile(const TileArgs& a, int sm_count) {
     if (a.prefix_len) {
       pages = (double)((all + n - 1) / n) * a.prefix_blocks + 0.5 * a.batch * a.max_blocks * (1 + (a.rows - 1) / n);
     } else {
-      const double most = ((double)a.window + a.s_q - 1) / kPage + 2 + ((double)a.sinks + kPage - 1) / kPage;
-      pages = a.batch * std::min((double)a.max_blocks, std::floor(most)) * groups;
+      pages = (double)a.batch * most_pages(a, n) * groups;
     }
     const double t = fixed[i] + page[i] * std::max(2.0, pages / (n == 128 ? sm_count / 2 : sm_count));
     if (!tile || t < best) {
@@ -901,7 +1028,7 @@ void tile_schedule(TileArgs* a) {
   const int mp = knob_value(MLA_KNOB_MIN_PAGES), pc = knob_value(MLA_KNOB_PIECE_COST);
   const int policy = knob_value(MLA_KNOB_SPLIT_POLICY);
   a->granule = a->row_tile == 128 ? 2 : 1;  // pages per step
-  a->min_pages = mp > 0 ? mp : 2;
+  a->min_pages = mp > 0 ? mp : a->team ? 1 : 2;
   // A piece costs a pair as much as 10 of its pages, a single CTA, whose stores overlap, as much
   // as one (us at 4 / 7 / 10 / 13 pages: pair, 64 sequences of 128 heads sharing 8,192 tokens
   // 161 / 137 / 146 / 154, 32 sharing 2,000 44 / 37 / 36 / 38; single, at 0 / 1 / 2 / 3, 16
@@ -922,7 +1049,7 @@ cudaError_t launch_decode_tile(const TileArgs& a, cudaStream_t stream) {
   if (a.row_tile == 128) e = launch_decode_tile_pair(a, stream);
   else if (shared) e = a.row_tile == 16 ? launch_tile<16, true>(a, stream) : launch_tile<32, true>(a, stream);
   else e = a.row_tile == 16 ? launch_tile<16, false>(a, stream) : launch_tile<32, false>(a, stream);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || a.team) return e;
   // As many CTAs as run at once; each takes rows until they are done.
   const int R = a.batch * a.rows;
   if (R <= 2 * a.sm_count)

@@ -781,7 +781,7 @@ cudaError_t launch_pair(const TileArgs& a, cudaStream_t stream) {
   if (!tile_maps(a, 64, kQSmemBoxes, &kv_map, &rope_map, &q_map)) return cudaErrorInvalidValue;
   const uint64_t limit_ns = (uint64_t)a.wait_limit * 1000000ull;
   return launch_dependent(decode_tile_pair_kernel<kShared, kMixed>, 2 * a.num_workers * (kShared ? 1 : a.groups), kThreads,
-                          kAlloc, stream, kv_map, rope_map, q_map, a, limit_ns);
+                          kAlloc, 0, stream, kv_map, rope_map, q_map, a, limit_ns);
 }
 
 }  // namespace

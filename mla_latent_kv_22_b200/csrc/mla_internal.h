@@ -125,6 +125,7 @@ struct TileArgs {
   float scale;
   int* err;
   int row_tile, groups, tiles;
+  int team;  // CTAs per row tile of a short call, a cluster that also merges its pieces; 0 = the split schedule
   // Workspace: a record per task; split partials [2 workers][groups (window) or 1][row_tile].
   SeqInfo* task;
   float* part_lse;

@@ -226,3 +226,90 @@ def test_pairs_on_two_streams_and_in_a_graph():
     for (o, l), (eo, el) in zip(outs, eager):
         assert torch.equal(o, eo) and torch.equal(l, el)
     del g
+
+
+# Short calls: clusters that merge their own pieces, up to as many as run at once and above.
+@pytest.mark.parametrize("B", [1, 2, 6, 7, 8, 14, 16])
+@pytest.mark.parametrize("H,s_q,window,sinks", [(16, 1, 60, 0), (16, 1, 400, 5), (9, 3, 700, 64), (64, 1, 500, 4)])
+def test_short_windows(B, H, s_q, window, sinks):
+    lens = [(900, 0, 1, 64, 65, 3000, 129, 450)[i % 8] for i in range(B)]
+    c, q = window_case(lens, s_q, H, window, sinks, seed=800 + B)
+    good = ref(c, q, window, sinks)
+    out, lse, err = run(c, q, window, sinks)
+    assert err == 0
+    assert_rounded(out, lse, good)
+    o2, l2, _ = run(c, q, window, sinks)
+    assert torch.equal(out, o2) and torch.equal(lse, l2)
+    c.block_table[0, 899 // 64] = c.kv_cache.shape[0]
+    skip = (0,) if B < 4 else (0, 3)
+    if B > 3:
+        c.cache_seqlens[3] = -5
+    out, lse, err = run(c, q, window, sinks)
+    assert err == 5
+    want, keep = but(good, skip, B)
+    if keep:
+        assert_rounded(out[keep], lse[keep], want)
+    for b in skip:
+        assert torch.isnan(out[b]).all() and torch.isnan(lse[b]).all()
+
+
+@pytest.mark.parametrize("B,H,P,most", [(1, 16, 400, 60), (7, 16, 700, 250), (14, 16, 130, 64), (16, 8, 300, 200), (9, 5, 200, 100)])
+def test_short_shared_prefixes(B, H, P, most):
+    lens = [int(x) for x in np.random.default_rng(B).integers(0, most + 1, B)]
+    c = Shared(P, lens, 1, H, seed=820 + B)
+    good = c.ref()
+    out, lse, err = c.run()
+    assert err == 0
+    assert_rounded(out, lse, good)
+    c.lens[B - 1] = 64 * c.table.shape[1] + 1
+    out, lse, err = c.run()
+    assert err == 5 and torch.isnan(out[B - 1]).all() and torch.isnan(lse[B - 1]).all()
+    want, keep = but(good, (B - 1,), B)
+    if keep:
+        assert_rounded(out[keep], lse[keep], want)
+    c.lens[B - 1], c.P = lens[B - 1], -1
+    out, lse, err = c.run()
+    assert err == 5 and torch.isnan(out).all() and torch.isnan(lse).all()
+
+
+def test_a_short_call_times_out_and_the_context_survives():
+    c, q = window_case([900, 300], 1, 16, 500, 4, seed=840)
+    M.mla_set_knob("wait_limit", 200)
+    M.mla_set_knob("withhold_arrive", 1)
+    assert run(c, q, 500, 4)[2] == 6
+    M.mla_set_knob("withhold_arrive", 0)
+    out, lse, err = run(c, q, 500, 4)
+    assert err == 0
+    assert_rounded(out, lse, ref(c, q, 500, 4))
+
+
+def test_short_calls_on_streams_and_replayed_with_other_lengths():
+    # Three at a time, each with up to 14 clusters: more than run at once.
+    from gpu_helpers import bf16_dev
+    T = [900, 64, 3000, 5, 400, 1, 777, 300, 500, 128, 129, 640, 33, 1000]
+    c, q = window_case(T, 1, 16, 10 ** 6, 0, seed=841)
+    dq, kv, bt = bf16_dev(q), bf16_dev(c.kv_cache), torch.from_numpy(c.block_table).cuda()
+    sl = torch.from_numpy(c.cache_seqlens).cuda()
+    windows, streams = (100, 500, 640), [torch.cuda.Stream() for _ in range(3)]
+    outs = [(torch.empty(14, 1, 16, 512, dtype=torch.bfloat16, device="cuda"), torch.empty(14, 1, 16, device="cuda")) for _ in windows]
+    call = lambda i, st=None: M.mla_decode_window(dq, kv, bt, sl, *outs[i], c.softmax_scale, windows[i], 2, stream=st)
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for i, st in enumerate(streams):
+            call(i, st)
+    torch.cuda.synchronize()
+    for w, o in zip(windows, outs):
+        assert_rounded(*o, ref(c, q, w, 2), f"window {w}")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for i in (0, 1, 2, 1):
+            call(i)
+    c.cache_seqlens[:] = [max(0, t - 70 * (i % 3)) for i, t in enumerate(T)]
+    sl.copy_(torch.from_numpy(c.cache_seqlens))
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    assert M.mla_get_device_error() == 0
+    for w, o in zip(windows, outs):
+        assert_rounded(*o, ref(c, q, w, 2), f"window {w}, replayed")
+    del g
