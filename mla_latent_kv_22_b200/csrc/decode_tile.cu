@@ -343,9 +343,11 @@ __global__ void __launch_bounds__(kCombineThreads, 3) combine_tile_kernel(const 
 // evenly and merges its pieces itself, behind a barrier of the cluster instead of in a second
 // grid.  Such a call is a chain of latencies (lengths, table, page, the two products, store,
 // merge); the team takes the second grid's start and the exchange over the batch's lengths
-// out of it, and its launch off the host (9.7 -> 5.9 us a call).  us, split schedule / team of 8 / of 16: 16 heads over a window of 512 10.6 /
-// 10.9 / 10.0, of 64 11.8 / 9.4 / 9.5; 2 such windows of 512 11.5 / 11.1 / 10.0, 14 of them
-// 13.4 / 11.9 / -; 7 sequences of 16 heads behind 1,000 tokens 14.0 / 13.7 / 13.4.
+// out of it, and its launch off the host (9.7 -> 5.9 us a call).  us, split schedule / team of
+// 8 / of 16: 16 heads over a window of 512 10.6 / 10.9 / 10.0, of 64 11.8 / 9.4 / 9.5; 2 such
+// windows of 512 11.5 / 11.1 / 10.0, 14 of them 13.4 / 11.9 / -; 7 sequences of 16 heads behind
+// 1,000 tokens 14.0 / 13.7 / 13.4.  (Pieces left in shared memory and read across the cluster
+// took 10.4 for 9.7: every CTA has to stay until its peers have read.)
 
 // The team's record of tile (t, grp), and this CTA's range of its pages.
 template <bool kShared>
@@ -364,14 +366,14 @@ static __device__ __noinline__ void team_range(const TileArgs& a, int t, int ran
   __syncthreads();
 }
 
-// The team's rows, eight CTAs by three groups of 128 threads at a time.
+// The team's rows, three per CTA at a time, with all pieces of a row in flight.
 template <int N, bool kShared>
 static __device__ __noinline__ void team_merge(const TileArgs& a, int t, int grp, int rank, const SeqInfo& s) {
   const Task k = load_task<N, kShared>(a, t, grp);
 #pragma unroll 1
   for (int row = rank + a.team * (threadIdx.x >> 7); row < k.live; row += a.team * (kThreads / 128)) {
     const int gr = k.row0 + row, b = gr / a.rows;
-    merge_row<kShared, 1, 8>(a, gr, b, gr - b * a.rows, s, 0, static_cast<MergeScratch<1>*>(nullptr));
+    merge_row<kShared, 1, 16>(a, gr, b, gr - b * a.rows, s, 0, static_cast<MergeScratch<1>*>(nullptr));
   }
 }
 
