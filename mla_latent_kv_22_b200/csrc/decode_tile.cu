@@ -985,10 +985,10 @@ int pick_row_tile(const TileArgs& a, int sm_count) {
   const int forced = knob_value(MLA_KNOB_ROW_TILE);
   for (int n : kRowTiles)
     if (forced == n) return n;
-  // us: of a call, and of a page per worker, fitted to 39 shapes (us at 16 / 32 / 128 rows a
-  // tile: a window of 512 for 128 heads 11.6 / 11.7 / 15.5, 64 windows of 1,024 for 64 heads
-  // 58 / 37 / 27; 7 sequences of 16 heads behind 1,000 tokens 13.4 / 14.2 / 17.5, 16 behind
-  // 16,000 44 / 32 / 25; tiles of 64 rows on one CTA were best nowhere).
+  // us: of a call, and of a page per worker, fitted to 39 shapes of the split schedule (us at
+  // 16 / 32 / 128 rows a tile: a window of 512 for 128 heads 11.6 / 11.7 / 15.5, 64 windows of
+  // 1,024 for 64 heads 58 / 37 / 27; 7 sequences of 16 heads behind 1,000 tokens 13.4 / 14.2 /
+  // 17.5, 16 behind 16,000 44 / 32 / 25; tiles of 64 rows on one CTA were best nowhere).
   const double fixed[] = {10.2, 10.8, 14.3}, page[] = {1.5, 1.7, 0.8};
   const long long all = a.prefix_len ? (long long)a.batch * a.rows : a.rows;
   double best = 0;
