@@ -274,6 +274,10 @@ mla_status_t mla_decode_window(const void* q, const void* kv_cache, const int32_
  * q, out, lse, s_q, heads, softmax_scale, workspace, empty queries, errors, sight: as in
  * mla_decode_window (prefix_blocks counts like max_blocks; an invalid prefix_len makes every
  * row NaN, an invalid length or own page the rows of its sequence).
+ * The host sees the tables' widths, not the lengths.  Spare columns of block_table may cost a
+ * short call 3 to 6 % (7 sequences of 16 heads behind 1,000 tokens 12.9 us with exact tables,
+ * 13.3 to 13.8 with 512 columns: the split of short calls is only for tables that cannot hold many
+ * pages); longer calls take the same time.
  */
 size_t mla_decode_shared_workspace_size(int batch, int s_q, int heads);
 mla_status_t mla_decode_shared(const void* q, const void* kv_cache, const int32_t* prefix_table, const int32_t* prefix_len,

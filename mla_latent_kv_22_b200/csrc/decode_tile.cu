@@ -977,38 +977,46 @@ size_t lay_out(TileArgs* a, int row_tile, int sm_count, int forced_workers, void
   return off;
 }
 
+// Estimated us of a call in tiles of kRowTiles[i] rows: a call's own, and a page's per worker,
+// fitted to 39 shapes of the split schedule (us at 16 / 32 / 128 rows a tile: a window of 512 for
+// 128 heads 11.6 / 11.7 / 15.5, 64 windows of 1,024 for 64 heads 58 / 37 / 27; 7 sequences of 16
+// heads behind 1,000 tokens 13.4 / 14.2 / 17.5, 16 behind 16,000 44 / 32 / 25; tiles of 64 rows on
+// one CTA were best nowhere).  The pages are those that the window or the prefix's table allow,
+// and, behind a shared prefix, `own` of each sequence.
+double tile_time(const TileArgs& a, int i, int sm_count, double own) {
+  constexpr double fixed[] = {10.2, 10.8, 14.3}, page[] = {1.5, 1.7, 0.8};
+  const int n = kRowTiles[i];
+  double pages;
+  if (a.prefix_len)
+    pages = (double)(((long long)a.batch * a.rows + n - 1) / n) * a.prefix_blocks + own * a.batch * (1 + (a.rows - 1) / n);
+  else
+    pages = (double)a.batch * most_pages(a, n) * ((a.rows + n - 1) / n);
+  return fixed[i] + page[i] * std::max(2.0, pages / (n == 128 ? sm_count / 2 : sm_count));
+}
+
 // The row tile with the least estimated time.  A narrow tile costs more per row and page, but
 // spreads the fixed parts of a short call (above all the partials' stores, at 32 bytes a cycle
-// and SM) over more SMs.  The pages are those that the window or the tables allow, half of the
-// own pages of a shared prefix.
+// and SM) over more SMs.  The host does not know the lengths, and a server's tables may be as
+// wide as its longest allowed sequence: behind a shared prefix the tile that serves both few own
+// pages (4 a sequence) and many (half the table) is taken, by the sum of its times over the best
+// ones.  (By half the table alone, 2,048 columns swamped the prefix: 64 sequences of 16 heads
+// with up to 200 tokens behind 4,096 took 46.9 us in 16-row tiles for 27 in 128-row ones, 32 with
+// up to 300 behind 4,000 33.5 for 24.  By the estimate over 20,000 drawn shapes with 2,048
+// columns, the choice costs at most 1.2 times the best one's time, 4.6 times by half the table.)
 int pick_row_tile(const TileArgs& a, int sm_count) {
   const int forced = knob_value(MLA_KNOB_ROW_TILE);
   for (int n : kRowTiles)
     if (forced == n) return n;
-  // us: of a call, and of a page per worker, fitted to 39 shapes of the split schedule (us at
-  // 16 / 32 / 128 rows a tile: a window of 512 for 128 heads 11.6 / 11.7 / 15.5, 64 windows of
-  // 1,024 for 64 heads 58 / 37 / 27; 7 sequences of 16 heads behind 1,000 tokens 13.4 / 14.2 /
-  // 17.5, 16 behind 16,000 44 / 32 / 25; tiles of 64 rows on one CTA were best nowhere).
-  const double fixed[] = {10.2, 10.8, 14.3}, page[] = {1.5, 1.7, 0.8};
-  const long long all = a.prefix_len ? (long long)a.batch * a.rows : a.rows;
-  double best = 0;
-  int tile = 0;
-  for (int i = 0; i < (all <= 16 ? 1 : 3); ++i) {
-    const int n = kRowTiles[i];
-    const double groups = (a.rows + n - 1) / n;
-    double pages;
-    if (a.prefix_len) {
-      pages = (double)((all + n - 1) / n) * a.prefix_blocks + 0.5 * a.batch * a.max_blocks * (1 + (a.rows - 1) / n);
-    } else {
-      pages = (double)a.batch * most_pages(a, n) * groups;
-    }
-    const double t = fixed[i] + page[i] * std::max(2.0, pages / (n == 128 ? sm_count / 2 : sm_count));
-    if (!tile || t < best) {
-      best = t;
-      tile = n;
-    }
+  if ((a.prefix_len ? (long long)a.batch * a.rows : a.rows) <= 16) return 16;
+  double loss[3] = {};
+  const double many = 0.5 * a.max_blocks;
+  for (double own : {std::min(4.0, many), many}) {
+    double t[3];
+    for (int i = 0; i < 3; ++i) t[i] = tile_time(a, i, sm_count, own);
+    const double best = *std::min_element(t, t + 3);
+    for (int i = 0; i < 3; ++i) loss[i] += t[i] / best;
   }
-  return tile;
+  return kRowTiles[std::min_element(loss, loss + 3) - loss];
 }
 
 }  // namespace
