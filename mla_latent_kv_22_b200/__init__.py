@@ -5,15 +5,21 @@ shape, device and contiguity, and passes raw pointers, sizes and the current CUD
 stream to the C ABI of the same name (include/mla.h); every step of the
 computation runs in the library's CUDA kernels.  Importing fails loudly when the
 library has not been built (``python mla_latent_kv_22_b200/build.py``); there is
-no fallback.
+no fallback.  The short calls go through a compiled extension first where one is built
+for the running torch and Python; without it they make the same call through ctypes.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import operator
 import os
+import types
+import warnings
 
 import torch
+
+from .build import binding_path
 
 __all__ = [
     "MlaError", "mla_decode", "mla_decode_multi", "mla_decode_noalloc", "mla_absorb_q", "mla_absorb_o", "mla_append",
@@ -82,11 +88,26 @@ def _load() -> ctypes.CDLL:
 
 lib = _load()
 
-try:
-    from . import _binding  # the quick path of the short calls (csrc/binding.cpp)
-except ImportError as e:
-    raise ImportError(f"the compiled binding is missing or does not load ({e}): build it with "
-                      "`python mla_latent_kv_22_b200/build.py`") from e
+
+def _load_binding():
+    """The quick path of the short calls (csrc/binding.cpp), or, where it has not been built for
+    this torch and Python, functions that hand every call back to the code below."""
+    path, why = binding_path(), "is missing"
+    if os.path.exists(path):
+        try:
+            spec = importlib.util.spec_from_file_location(__name__ + "._binding", path)
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+            return module
+        except ImportError as e:
+            why = f"does not load ({e})"
+    warnings.warn(f"{path} {why}: the same kernels run, but short calls take longer on the host; build it with "
+                  "`python mla_latent_kv_22_b200/build.py`", RuntimeWarning, stacklevel=3)
+    decline = lambda *args: NotImplemented
+    return types.SimpleNamespace(decode_window=decline, decode_shared=decline, append=decline, absorb_o=decline)
+
+
+_binding = _load_binding()
 
 
 def _check(status: int) -> None:

@@ -1,5 +1,5 @@
-"""Builds libmla.so in-tree with nvcc for sm_100a (B200), and _binding.so, the binding's
-quick path, with g++ against torch's headers.
+"""Builds libmla.so in-tree with nvcc for sm_100a (B200), and the binding's quick path (an
+extension module named after the torch and Python it is for) with g++ against torch's headers.
 
     python mla_latent_kv_22_b200/build.py [--force] [--verbose] [--ptxas]
 
@@ -19,7 +19,6 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmla.so")
-BINDING = os.path.join(PKG, "_binding.so")
 BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 
 NVCC_FLAGS = [
@@ -44,8 +43,17 @@ def _newer(target: str, deps: list[str]) -> bool:
     return os.path.exists(target) and all(os.path.getmtime(p) <= os.path.getmtime(target) for p in deps)
 
 
+def binding_path() -> str:
+    """The quick path's extension for the running Python and torch.  It reads torch's C++
+    objects, so one built for another version must never be loaded: each has a file of its own."""
+    import torch
+
+    tag = f"torch-{torch.__version__}-abi{int(torch._C._GLIBCXX_USE_CXX11_ABI)}"
+    return os.path.join(PKG, f"_binding.{tag}{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
 def _binding_up_to_date() -> bool:
-    return _newer(BINDING, [BINDING_SRC] + glob.glob(os.path.join(INCLUDE, "*.h")))
+    return _newer(binding_path(), [BINDING_SRC] + glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
 def up_to_date() -> bool:
@@ -75,13 +83,13 @@ def _run(cmd: list[str], target: str, verbose: bool) -> None:
 def _build_binding(verbose: bool) -> None:
     import torch
 
-    T = os.path.dirname(torch.__file__)
+    T, target = os.path.dirname(torch.__file__), binding_path()
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
     _run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
           "-I", INCLUDE, "-isystem", os.path.join(T, "include"), "-isystem", os.path.join(T, "include/torch/csrc/api/include"),
-          "-isystem", sysconfig.get_paths()["include"], "-isystem", cuda, "-o", BINDING + ".tmp", BINDING_SRC, "-L", PKG, "-l:libmla.so",
+          "-isystem", sysconfig.get_paths()["include"], "-isystem", cuda, "-o", target + ".tmp", BINDING_SRC, "-L", PKG, "-l:libmla.so",
           "-L", os.path.join(T, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
-          "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + os.path.join(T, "lib")], BINDING, verbose)
+          "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + os.path.join(T, "lib")], target, verbose)
 
 
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
