@@ -28,6 +28,7 @@ struct DeviceState {
   bool init = false;
   int sm_count = 0;
   int* err = nullptr;           // device address of g_device_error
+  cudaStream_t side = nullptr;  // reads and clears it, in the order of no other stream
   void* ws = nullptr;           // workspace base
   size_t ws_bytes = 0;
   bool ws_external = false;     // set by mla_set_workspace
@@ -256,19 +257,30 @@ mla_status_t mla_set_workspace(void* dev_ptr, size_t bytes) {
 }
 
 mla_status_t mla_get_device_error(mla_stream_t stream) {
-  std::lock_guard<std::mutex> lk(g_mu);
+  // The wait holds no lock: other threads' calls go on meanwhile (the stream may even depend on
+  // work that they have yet to submit).
   DeviceState* d = nullptr;
-  mla_status_t s = device_state(&d);
-  if (s != MLA_OK) return s;
+  {
+    std::lock_guard<std::mutex> lk(g_mu);
+    mla_status_t s = device_state(&d);
+    if (s != MLA_OK) return s;
+    if (!d->side) {
+      const cudaError_t e = cudaStreamCreateWithFlags(&d->side, cudaStreamNonBlocking);
+      if (e != cudaSuccess) return cuda_fail(e, "cudaStreamCreate");
+    }
+  }
   cudaError_t e = cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "cudaStreamSynchronize");
+  std::lock_guard<std::mutex> lk(g_mu);
   int v = 0;
-  e = cudaMemcpy(&v, d->err, sizeof(int), cudaMemcpyDeviceToHost);
+  e = cudaMemcpyAsync(&v, d->err, sizeof(int), cudaMemcpyDeviceToHost, d->side);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(d->side);
   if (e != cudaSuccess) return cuda_fail(e, "read error word");
-  const int zero = 0;
-  e = cudaMemcpy(d->err, &zero, sizeof(int), cudaMemcpyHostToDevice);
-  if (e != cudaSuccess) return cuda_fail(e, "clear error word");
   if (v == 0) return MLA_OK;
+  const int zero = 0;
+  e = cudaMemcpyAsync(d->err, &zero, sizeof(int), cudaMemcpyHostToDevice, d->side);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(d->side);
+  if (e != cudaSuccess) return cuda_fail(e, "clear error word");
   return v == MLA_ERR_DEVICE_TIMEOUT        ? MLA_ERR_DEVICE_TIMEOUT
          : v == MLA_ERR_DEVICE_BAD_POSITION ? MLA_ERR_DEVICE_BAD_POSITION
                                             : MLA_ERR_DEVICE_BAD_PAGE;

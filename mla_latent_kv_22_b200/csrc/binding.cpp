@@ -4,6 +4,9 @@
 // wrong argument, another device, a non-contiguous tensor) is handed back as NotImplemented to
 // the Python code, which accepts it or says what is wrong.
 //
+// The library is entered without the interpreter's lock, as ctypes does: it may wait for another
+// thread that holds the library's.
+//
 // Host time per call, Python code / this (us): append 11.3 / 2.9, window decode 15.8 / 8.4
 // (6.2 of it two launches and three tensor maps; 5.9 a short one, of one launch), value
 // absorption 6.4 / 3.5.
@@ -105,7 +108,14 @@ struct Cache {
   }
 };
 
-PyObject* status(mla_status_t s) {
+// The status of a call into the library, made without the interpreter's lock; its arguments are
+// plain values by then.
+template <typename Call>
+PyObject* status(const Call& call) {
+  mla_status_t s;
+  Py_BEGIN_ALLOW_THREADS
+  s = call();
+  Py_END_ALLOW_THREADS
   if (s == MLA_OK) Py_RETURN_NONE;
   return PyLong_FromLong(s);
 }
@@ -154,8 +164,11 @@ PyObject* decode_window(PyObject*, PyObject* const* p, Py_ssize_t n) {
   if (!a.ok) return not_mine();
   const size_t bytes = mla_decode_window_workspace_size((int)x.B, (int)x.SQ, (int)x.H);
   const at::DataPtr ws = scratch(bytes);
-  return status(mla_decode_window(x.q, c.kv, c.table, x.lens, x.out, x.lse, (int)x.B, (int)x.SQ, (int)x.H, c.num_pages,
-                                  c.max_blocks, (int)window, (int)sinks, (float)scale, ws.get(), bytes, a.stream()));
+  const mla_stream_t stream = a.stream();
+  return status([&] {
+    return mla_decode_window(x.q, c.kv, c.table, x.lens, x.out, x.lse, (int)x.B, (int)x.SQ, (int)x.H, c.num_pages, c.max_blocks,
+                             (int)window, (int)sinks, (float)scale, ws.get(), bytes, stream);
+  });
   END_HANDLE_TH_ERRORS
 }
 
@@ -173,9 +186,13 @@ PyObject* decode_shared(PyObject*, PyObject* const* p, Py_ssize_t n) {
   if (!a.ok || pt->dim() != 1 || !pt->is_contiguous() || pt->size(0) > INT32_MAX) return not_mine();
   const size_t bytes = mla_decode_shared_workspace_size((int)x.B, (int)x.SQ, (int)x.H);
   const at::DataPtr ws = scratch(bytes);
-  return status(mla_decode_shared(x.q, c.kv, static_cast<const int32_t*>(pt->data_ptr()), plen, c.table, x.lens, x.out, x.lse,
-                                  (int)x.B, (int)x.SQ, (int)x.H, c.num_pages, (int)pt->size(0), c.max_blocks, (float)scale,
-                                  ws.get(), bytes, a.stream()));
+  const int32_t* const prefix = static_cast<const int32_t*>(pt->data_ptr());
+  const int prefix_blocks = (int)pt->size(0);
+  const mla_stream_t stream = a.stream();
+  return status([&] {
+    return mla_decode_shared(x.q, c.kv, prefix, plen, c.table, x.lens, x.out, x.lse, (int)x.B, (int)x.SQ, (int)x.H, c.num_pages,
+                             prefix_blocks, c.max_blocks, (float)scale, ws.get(), bytes, stream);
+  });
   END_HANDLE_TH_ERRORS
 }
 
@@ -207,9 +224,15 @@ PyObject* append(PyObject*, PyObject* const* p, Py_ssize_t n) {
   const Cache c(a, p[2], p[3], B);
   if (!a.ok || N > INT32_MAX || B > INT32_MAX || H > INT32_MAX || cs->size(0) > INT32_MAX || (p[10] != Py_True && p[10] != Py_False))
     return not_mine();
-  return status(mla_append(c_kv, k_rope, q, qo, static_cast<const float*>(cs->data_ptr()), cu, static_cast<const int32_t*>(l->data_ptr()),
-                           off, c.table, c.kv, sc[0], sk[0], sq[0], sq[1], so[0], so[1], (int)N, (int)B, (int)H, c.num_pages,
-                           c.max_blocks, (int)cs->size(0), p[10] == Py_True, a.stream()));
+  const float* const cos_sin = static_cast<const float*>(cs->data_ptr());
+  const int32_t* const lens = static_cast<const int32_t*>(l->data_ptr());
+  const int64_t st[6] = {sc[0], sk[0], sq[0], sq[1], so[0], so[1]};
+  const int max_pos = (int)cs->size(0), interleaved = p[10] == Py_True;
+  const mla_stream_t stream = a.stream();
+  return status([&] {
+    return mla_append(c_kv, k_rope, q, qo, cos_sin, cu, lens, off, c.table, c.kv, st[0], st[1], st[2], st[3], st[4], st[5], (int)N,
+                      (int)B, (int)H, c.num_pages, c.max_blocks, max_pos, interleaved, stream);
+  });
   END_HANDLE_TH_ERRORS
 }
 
@@ -224,7 +247,8 @@ PyObject* absorb_o(PyObject*, PyObject* const* p, Py_ssize_t n) {
   void *x = a.dense(p[0], at::kBFloat16, {B, H, kLatent}), *w = a.dense(p[1], at::kBFloat16, {H, kLatent, kV});
   float* out = static_cast<float*>(a.dense(p[2], at::kFloat, {B, H, kV}));
   if (!a.ok || B > INT32_MAX || H > INT32_MAX) return not_mine();
-  return status(mla_absorb_o_bf16(x, w, out, (int)B, (int)H, a.stream()));
+  const mla_stream_t stream = a.stream();
+  return status([&] { return mla_absorb_o_bf16(x, w, out, (int)B, (int)H, stream); });
   END_HANDLE_TH_ERRORS
 }
 
