@@ -111,13 +111,19 @@ struct Ctl {
 };
 
 // Bounded wait on an mbarrier phase; false on timeout (recorded) or abort.  The first try is
-// inlined, the rest is not (it would be at some thirty places).  CTA-scope
-// acquire: what crosses the pair is read by the tensor cores alone.
+// inlined, the rest is not (it would be at some thirty places).  CTA-scope acquire, since what
+// crosses the pair is read by the tensor cores alone; kCluster: but for drop_s, whose words the
+// peer's warps set and the value MMAs' warp reads.
+template <bool kCluster>
+__device__ __forceinline__ bool phase_done(uint32_t bar, uint32_t parity) {
+  return kCluster ? mbar_try_wait(bar, parity) : mbar_try_wait_cta(bar, parity);
+}
+template <bool kCluster>
 __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, Ctl* c) {
   uint64_t t0 = 0;
 #pragma unroll 1
   for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait_cta(bar, parity)) return true;
+    if (phase_done<kCluster>(bar, parity)) return true;
     if ((i & 63) == 0) {
       if (*const_cast<volatile int*>(&c->abort)) return false;
       const uint64_t t = now_ns();
@@ -132,8 +138,9 @@ __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, Ctl* c) {
     }
   }
 }
+template <bool kCluster = false>
 __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, Ctl* c) {
-  return __all_sync(0xffffffffu, mbar_try_wait_cta(bar, parity) || wait_long(bar, parity, c));
+  return __all_sync(0xffffffffu, phase_done<kCluster>(bar, parity) || wait_long<kCluster>(bar, parity, c));
 }
 __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
   const uint64_t t0 = now_ns();
@@ -511,7 +518,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       while (ok && pi.next(pc, a)) {
         const int steps = (pc.pe - pc.pa + 1) / 2;
         for (int i = 0; i < steps && ok; ++i, ++g) {
-          if (!wait_all(bar(kPFull), g & 1, ctl) ||
+          if (!wait_all<kMixed>(bar(kPFull), g & 1, ctl) ||
               (i == 0 && piece > 0 && !wait_all(bar(kOFree), (piece - 1) & 1, ctl))) {
             ok = false;
             break;
@@ -519,10 +526,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if constexpr (kMixed) {
             const uint32_t drop = reinterpret_cast<volatile uint32_t*>(drop_s[g & 3])[lane & 3];
             if (__any_sync(0xffffffffu, drop)) {
+              if (lane < 4) drop_s[g & 3][lane] = 0;  // before the fences of drop_values: set again four steps on
               if (!wait_all(bar(kFullV), g & 1, ctl) || !wait_all(bar(kFullV + 1), g & 1, ctl)) { ok = false; break; }
               drop_values(sbase + kOffV, drop, lane);
-              if (lane < 4) drop_s[g & 3][lane] = 0;
-              __syncwarp();
             }
           }
           tc_fence_after();
