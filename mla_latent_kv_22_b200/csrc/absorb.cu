@@ -617,10 +617,11 @@ __global__ void __launch_bounds__(kXThreads, 1)
     const bool live = !kHalf || lane < 16;
     const uint32_t t_row = tmem + ((uint32_t)(32 * q) << 16);
     int it = 0;
+    bool ok = true;  // no wait ran out: the outputs of this CTA's remaining items are NaN then
     for (int item = blockIdx.x; item < items; item += gridDim.x, ++it) {
       const int hp = item % (H * kParts), h = hp / kParts, v0 = kM * (hp % kParts), b0 = (item / (H * kParts)) * N;
       const int d = it & 1;
-      if (!__all_sync(0xffffffffu, wait_on(bar(kXDFull + d), (it >> 1) & 1, gd))) break;
+      ok = ok && __all_sync(0xffffffffu, wait_on(bar(kXDFull + d), (it >> 1) & 1, gd));
       tc_fence_after();
       float* dst = out + ((size_t)b0 * H + h) * MLA_D_V + v0 + v;
       const int rows = min(N, B - b0);
@@ -630,11 +631,11 @@ __global__ void __launch_bounds__(kXThreads, 1)
         tmem_wait_ld();
 #pragma unroll
         for (int e = 0; e < 16; ++e)
-          if (live && c + e < rows) dst[(size_t)(c + e) * H * MLA_D_V] = __uint_as_float(r[e]);
+          if (live && c + e < rows) dst[(size_t)(c + e) * H * MLA_D_V] = ok ? __uint_as_float(r[e]) : NAN;
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kXDEmpty + d));
+      if (ok && lane == 0) mbar_arrive(bar(kXDEmpty + d));
     }
   }
 

@@ -36,7 +36,8 @@
 // fp32; out is rounded once to bf16.
 //
 // Every mbarrier wait is bounded by a time limit; on expiry the kernel records
-// MLA_ERR_DEVICE_TIMEOUT, drains its work in flight and returns.  No trap.
+// MLA_ERR_DEVICE_TIMEOUT, drains its work in flight, makes the rows of its pieces NaN and
+// returns.  No trap.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -855,6 +856,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
+  if (ctl_s.abort) spoil_pieces<N, kShared>(a, range_s.rg, w, grp);
   if constexpr (kTeam) {
     __syncwarp();
     cluster_sync();  // the team's partials are written

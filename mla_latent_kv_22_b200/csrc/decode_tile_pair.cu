@@ -776,6 +776,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc_pair(tmem, kTmemCols);
   }
+  if (ctl_s.abort) spoil_pieces<kRows, kShared>(a, range_s.rg, w, grp);  // set in both CTAs
 }
 
 template <bool kShared, bool kMixed>

@@ -250,6 +250,29 @@ __device__ __forceinline__ PieceOut piece_out(const TileArgs& a, const Task& k, 
   return {false, (kShared ? slot : slot * a.groups + grp) * N};
 }
 
+// NaN for the rows of all pieces of a worker, one of whose waits ran out: written where the
+// piece's results go, or, for a partial, as the lse by which the merge makes its rows NaN.  By the
+// whole CTA, when nothing of it writes any more.
+template <int N, bool kShared>
+static __device__ __noinline__ void spoil_pieces(const TileArgs& a, const volatile WorkerRange& rg, int w, int grp) {
+  const int lane = threadIdx.x & 31;
+  PieceIter<kShared> it(rg);
+  Piece pc;
+#pragma unroll 1
+  while (it.next(pc, a)) {
+    const Task k = load_task<N, kShared>(a, pc.t, grp);
+    const PieceOut to = piece_out<N, kShared>(a, k, pc, it.rg, w, grp);
+#pragma unroll 1
+    for (int row = threadIdx.x >> 5; row < k.live; row += blockDim.x >> 5) {
+      if (lane == 0) (to.direct ? a.lse : a.part_lse)[to.row0 + row] = NAN;
+      if (to.direct) {
+        uint4* o = reinterpret_cast<uint4*>(a.out + (to.row0 + row) * kDLatent) + lane;
+        o[0] = o[32] = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+      }
+    }
+  }
+}
+
 // Whether some row of a page is in no query's sight.
 template <bool kShared>
 __device__ __forceinline__ bool page_dirty(const Task& k, const PageRef& r) {
