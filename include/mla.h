@@ -199,8 +199,9 @@ mla_status_t mla_decode_noalloc(const void* q, const void* kv_cache, const int32
  * k_rope     device bf16 [tokens, 64], k_rope_stride elements apart
  * q_rope     device bf16 [tokens, heads, 64] with strides q_stride_token, q_stride_head, or
  *            NULL (then q_out is NULL and heads is ignored)
- * q_out      device bf16, likewise with its own strides; may be q_rope itself with the
- *            same strides (rotation in place), and must not overlap it otherwise
+ * q_out      device bf16, likewise with its own strides, its vectors apart from one another;
+ *            may be q_rope itself with the same strides (rotation in place), and must not
+ *            overlap it otherwise
  * cos_sin    device fp32 [max_pos, 64]: 32 cosines, then 32 sines, of each position
  * cu_tokens  device int32 [batch + 1], ascending: sequence b's new tokens are
  *            cu_tokens[b] .. cu_tokens[b+1] (none is allowed); tokens at or beyond

@@ -631,17 +631,21 @@ mla_status_t mla_append(const void* c_kv, const void* k_rope, const void* q_rope
   if (!cu_tokens && tokens % batch)
     return fail(MLA_ERR_INVALID_ARG, "%d tokens are not the same number for each of %d sequences (cu_tokens is null)", tokens, batch);
   if (interleaved != 0 && interleaved != 1) return fail(MLA_ERR_INVALID_ARG, "interleaved = %d", interleaved);
-  if (!aligned16(c_kv) || !aligned16(k_rope) || !aligned16(q_rope) || !aligned16(q_out) || !aligned16(cos_sin) || !aligned16(kv_cache))
-    return fail(MLA_ERR_INVALID_ARG, "c_kv, k_rope, q_rope, q_out, cos_sin and kv_cache must be 16-byte aligned");
-  if ((reinterpret_cast<uintptr_t>(cu_tokens) | reinterpret_cast<uintptr_t>(cache_seqlens) |
-       reinterpret_cast<uintptr_t>(pos_offset) | reinterpret_cast<uintptr_t>(block_table)) & 3u)
-    return fail(MLA_ERR_INVALID_ARG, "int32 arrays must be 4-byte aligned");
   // The stride of a single token or head is never used, and may be anything.
   if (tokens == 1) c_kv_stride = k_rope_stride = q_stride_token = q_out_stride_token = 0;
   if (heads == 1) q_stride_head = q_out_stride_head = 0;
   const int64_t strides[6] = {c_kv_stride, k_rope_stride, q_stride_token, q_stride_head, q_out_stride_token, q_out_stride_head};
   for (int i = 0; i < (q_rope ? 6 : 2); ++i)
     if (strides[i] % 8) return fail(MLA_ERR_INVALID_ARG, "strides must be multiples of 8 elements (16 bytes)");
+  const auto overlap = [](int n, int64_t stride) { return n > 1 && stride > -MLA_D_ROPE && stride < MLA_D_ROPE; };
+  if (q_rope && (overlap(tokens, q_out_stride_token) || overlap(heads, q_out_stride_head)))
+    return fail(MLA_ERR_INVALID_ARG, "q_out's vectors overlap (strides %lld, %lld)", (long long)q_out_stride_token,
+                (long long)q_out_stride_head);
+  if (!aligned16(c_kv) || !aligned16(k_rope) || !aligned16(q_rope) || !aligned16(q_out) || !aligned16(cos_sin) || !aligned16(kv_cache))
+    return fail(MLA_ERR_INVALID_ARG, "c_kv, k_rope, q_rope, q_out, cos_sin and kv_cache must be 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(cu_tokens) | reinterpret_cast<uintptr_t>(cache_seqlens) |
+       reinterpret_cast<uintptr_t>(pos_offset) | reinterpret_cast<uintptr_t>(block_table)) & 3u)
+    return fail(MLA_ERR_INVALID_ARG, "int32 arrays must be 4-byte aligned");
 
   std::lock_guard<std::mutex> lk(g_mu);
   DeviceState* d = nullptr;
