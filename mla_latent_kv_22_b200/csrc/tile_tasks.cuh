@@ -123,7 +123,7 @@ __device__ __forceinline__ Task load_task(const TileArgs& a, int t, int g) {
     k.cut = a.s_q - 1 - (k.row0 + k.live - 1 - k.b1 * a.rows) / a.heads;
     const int P = *a.prefix_len;
     // Every sequence but the last has its last query in the tile, which sees the whole prefix.
-    k.s = Span{k.b0 < k.b1 ? P : min(P, P + a.seqlens[k.b1] - k.cut), prefix_pages(a), 0, 0, 0, 0};
+    k.s = Span{k.b0 < k.b1 ? P : P + min(a.seqlens[k.b1] - k.cut, 0), prefix_pages(a), 0, 0, 0, 0};
   } else {
     k.srow = g * N;
     k.row0 = t * a.rows + k.srow;

@@ -124,3 +124,64 @@ def test_rows_beside_a_tiles_edge(tile, s_q, H):
     out, lse, err = d.run()
     assert err == 0
     assert_rounded(out, lse, d.ref())
+
+
+@pytest.mark.parametrize("tile", [0, 16, 32, 128])
+def test_the_most_rows_of_a_sequence(tile):
+    M.mla_set_knob("row_tile", tile)
+    c, q = window_case([150, 7], 16, 128, 60, 2, seed=940)   # 2,048 rows
+    out, lse, err = run(c, q, 60, 2)
+    assert err == 0
+    assert_rounded(out, lse, ref(c, q, 60, 2))
+    d = Shared(70, [3, 90], 16, 128, seed=941)
+    out, lse, err = d.run()
+    assert err == 0
+    assert_rounded(out, lse, d.ref())
+
+
+FIRST = """
+import torch
+import mla_latent_kv_22_b200 as M
+bf, i32 = dict(dtype=torch.bfloat16, device="cuda"), dict(dtype=torch.int32, device="cuda")
+B, H = 2, 16
+x = lambda *s: torch.randn(*s, device="cuda").bfloat16()
+kv, table, lens, cos_sin = x(8, 64, 576), torch.arange(8, **i32).view(2, 4), torch.tensor([200, 70], **i32), torch.randn(300, 64, device="cuda")
+new, q, w = x(B, 576), x(B, H, 576), x(H, 512, 128)
+ptab, plen = torch.tensor([1, 2], **i32), torch.tensor([100], **i32)
+
+def step():
+    M.mla_append(new[:, :512], new[:, 512:], kv, table, lens, cos_sin)
+    r = [torch.empty(B, H, 512, **bf), torch.empty(B, H, device="cuda"), torch.empty(B, H, 512, **bf), torch.empty(B, H, device="cuda"),
+         torch.empty(B, H, 128, device="cuda")]
+    M.mla_decode_window(q, kv, table, lens, r[0], r[1], 0.07, 90, 4)
+    M.mla_decode_shared(q, kv, ptab, plen, table, lens, r[2], r[3], 0.07)
+    M.mla_absorb_o(r[0], w, r[4])
+    return r
+
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    held = step()
+g.replay()
+want = step()
+torch.cuda.synchronize()
+assert M.mla_get_device_error() == 0
+assert all(torch.equal(a, b) for a, b in zip(held, want)) and all(torch.isfinite(a).all() for a in want)
+z = lambda *s, **k: torch.empty(*s, **k)
+M.mla_decode_window(z(0, H, 576, **bf), kv, z(0, 4, **i32), z(0, **i32), z(0, H, 512, **bf), z(0, H, device="cuda"), 0.07, 90)   # no sequence
+M.mla_decode_shared(z(0, H, 576, **bf), kv, ptab, plen, z(0, 4, **i32), z(0, **i32), z(0, H, 512, **bf), z(0, H, device="cuda"), 0.07)
+M.mla_absorb_o(z(0, H, 512, **bf), w, z(0, H, 128, device="cuda"))
+M.mla_append(z(0, 512, **bf), z(0, 64, **bf), kv, z(0, 4, **i32), z(0, **i32), cos_sin)
+assert M.mla_get_device_error() == 0
+del g
+print("same")
+"""
+
+
+def test_the_first_calls_of_a_process_may_be_captured():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.split() == ["same"], r.stderr[-2000:]
