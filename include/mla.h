@@ -36,7 +36,9 @@
  *     return a status before anything is launched.  Errors found on the device
  *     (a page id outside [0, num_pages), a bounded wait that ran out) set the
  *     per-device error word, read by mla_get_device_error; the affected
- *     sequences' outputs are NaN.  No kernel traps.
+ *     sequences' outputs are NaN.  (Of a call whose wait ran out, mla_decode,
+ *     mla_decode_multi, mla_decode_noalloc, mla_absorb_q and the fp32 mla_absorb_o
+ *     do not mark what they left undone: discard all its outputs.)  No kernel traps.
  *   - Fixed widths: latent 512, rope 64 (row 576), page 64 tokens, and for the
  *     absorption GEMMs 128 no-rope query dims and 128 value dims.  Heads 1..128.
  */
@@ -307,8 +309,9 @@ mla_status_t mla_set_workspace(void* dev_ptr, size_t bytes);
 
 /*
  * Synchronise `stream`, then read and clear the current device's error word.
- * Returns MLA_OK, MLA_ERR_DEVICE_BAD_PAGE or MLA_ERR_DEVICE_TIMEOUT (or
- * MLA_ERR_CUDA if the synchronisation itself failed).
+ * Returns MLA_OK, MLA_ERR_DEVICE_BAD_PAGE, MLA_ERR_DEVICE_TIMEOUT or
+ * MLA_ERR_DEVICE_BAD_POSITION, the first that was set (or MLA_ERR_CUDA if the
+ * synchronisation itself failed).  Other threads' calls go on during the wait.
  */
 mla_status_t mla_get_device_error(mla_stream_t stream);
 

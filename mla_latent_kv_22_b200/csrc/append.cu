@@ -7,10 +7,10 @@
 //
 // Bound by HBM: every input is read and every output written once (36 KB per token with
 // 128 heads, of which the query part is 32 KB), with no arithmetic to speak of.  One block
-// per token.  A thread keeps one eighth of a turn of the table (8 pairs: 16 fp32 values)
-// for its token and applies it to the same pairs of every 32nd head; all of a thread's
-// loads are issued before the token's sequence, position and page are looked up, so the
-// chain lengths -> page -> store hides behind them.
+// per token.  A thread keeps a quarter of its token's row of the table (8 pairs: 16 fp32
+// values) and applies it to the same pairs of every 32nd head; all of a thread's loads are
+// issued before the token's sequence, position and page are looked up, so the chain lengths
+// -> page -> store hides behind them.
 #include "mla_device.cuh"
 #include "mla_internal.h"
 

@@ -32,7 +32,7 @@
 // The running maximum is lazy as in decode_pair.cu: O and the sum are rescaled only when a
 // page's maximum exceeds the reference by more than 2^8.  Since O's lanes are dims, all
 // four warps rescale for a row of any of them; they meet once per page.  P is rounded to
-// bf16 (2^-9 relative) for the tensor cores; scores, sums, O and the split partials stay
+// bf16 (half a step: 2^-8 relative) for the tensor cores; scores, sums, O and the split partials stay
 // fp32; out is rounded once to bf16.
 //
 // Every mbarrier wait is bounded by a time limit; on expiry the kernel records
@@ -64,9 +64,9 @@ constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 0, kColS = 256;  // O^T: block m at column N m of its buffer; S: two buffers of 64 columns
 
-// Shared memory for a row tile of N: q' (9 boxes of [N rows x 64 dims]; twice where the
-// ring keeps its five slots, so that a piece's q' loads under the one before), P ([N rows
-// x 64 tokens], two buffers where they fit), two rope slots and the latent ring.
+// Shared memory for a row tile of N: q' (9 boxes of [N rows x 64 dims]; twice at 16 rows, so
+// that a piece's q' loads under the one before, once at 32, where five ring slots leave no
+// room), P ([N rows x 64 tokens], twice), two rope slots and the latent ring.
 template <int N>
 struct Layout {
   static constexpr int kQBox = N * 128;
@@ -476,9 +476,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int y = ld.row(p, dirty, bad_s[piece & 15]);
 #pragma unroll 1
         for (int m = 0; m < 2; ++m) {
-          // The page's rope rides on its second half, whose ring slot was last held by the
-          // page two before (4 or 5 slots): with that page's second product done, its
-          // scores are, and its rope slot is free.
+          // The page's rope rides on its second half, whose ring slot (of five) was last held
+          // by the first half of the page two before: with its second product done, that
+          // page's scores are, and its rope slot is free.
           if (!wait_all(bar(kEmpty + slot), phase, ctl)) { ok = false; break; }
           const uint32_t bit = 1u << slot;
           if (a.withhold_arrive && blockIdx.x == 0 && fills == 1) {
@@ -1042,7 +1042,7 @@ void tile_schedule(TileArgs* a) {
   a->granule = a->row_tile == 128 ? 2 : 1;  // pages per step
   a->min_pages = mp > 0 ? mp : a->team ? 1 : 2;
   // A piece costs a pair as much as 10 of its pages, a single CTA, whose stores overlap, as much
-  // as one (us at 4 / 7 / 10 / 13 pages: pair, 64 sequences of 128 heads sharing 8,192 tokens
+  // as one (graph-replayed us at 4 / 7 / 10 / 13 pages: pair, 64 sequences of 128 heads sharing 8,192 tokens
   // 161 / 137 / 146 / 154, 32 sharing 2,000 44 / 37 / 36 / 38; single, at 0 / 1 / 2 / 3, 16
   // heads over 256 windows of 1,021 67.3 / 67.2 / 68.3 / 69.2, over 200 of 4,096 143 / 142 /
   // 148 / 152, 8 sequences of 8 heads behind 4,000 tokens 16.1 / 15.0 / 15.0 / 15.0).
